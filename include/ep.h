@@ -21,6 +21,10 @@
  *       processes)
  *   ep_route_stats_noalloc (ep_route_stats with the library's own scratch)
  *
+ * and what stands around it in a model:
+ *   ep_router, ep_router_backward (router logits to topk_ids and w, and their
+ *       gradient)
+ *
  * Sources, cited by page title and section:
  *  [GR] "MoonEP: πώς η εξισορρόπηση των AI experts αλλάζει την υποδομή των MoE
  *       μοντέλων" (twodots.gr)
@@ -92,12 +96,17 @@ extern "C" {
 #define EP_DEV_BAD_LOADS 0x4         /* loads do not sum to R*S*K, or are negative */
 #define EP_DEV_BAD_ROW 0x8           /* a row index outside the buffer */
 #define EP_DEV_COPY_TIMEOUT 0x10     /* a bounded wait on an asynchronous copy gave up */
+#define EP_DEV_BAD_LOGIT 0x20        /* a router logit that is NaN or +infinity */
 
 #define EP_MAX_EXPERTS 1024
 #define EP_MAX_RANKS 1024
 
 #define EP_DTYPE_F32 0
 #define EP_DTYPE_BF16 1
+#define EP_DTYPE_F16 2 /* router logits only */
+
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
 
 /*
  * Layout of the plan buffer (int32 words) written by ep_plan.  Every field is an
@@ -618,6 +627,47 @@ EP_API int ep_quota_replica_grad_reduce_peer(float* g_home_local, const uint64_t
 #define EP_NOALLOC_SCRATCH_BYTES (4u << 20)
 EP_API int ep_route_stats_noalloc(const int32_t* topk_ids, int64_t T, int K, int E, int32_t* loads, double* max_vio,
                                   int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The router: logits of T tokens over E experts to the topk_ids and w that the
+ * path takes.  With x one token's logits, s = softmax(x) or sigmoid(x) element
+ * by element and b = bias (NULL: none):
+ *   key_e = s_e + b_e, or x_e without a bias;
+ *   groups: E / n_group consecutive experts form a group; its score is its
+ *     largest key (group_top 1) or the sum of its two largest (group_top 2;
+ *     without a bias the sum of its two largest s_e), over the experts that are
+ *     not masked; only experts of the topk_group best groups are taken;
+ *   topk_ids[t] = the K largest keys in descending order;
+ *   w[t,k] = scale * s_k, or with renorm != 0 scale * s_k / sum_j s_j.
+ * Equal keys, and equal group scores, go to the lower index; keys and group
+ * scores are compared in fp64.  The bias moves the choice only.
+ *   logits   [T, E] fp32, bf16 or fp16 (dtype), row t at t*ld elements, ld >= E.
+ *   bias     [E] fp32 or NULL.
+ *   topk_ids [T, K] int32 out, w [T, K] fp32 out.
+ * A logit of -inf masks its expert: s_e = 0, taken only after every expert that
+ * is not masked.  A row of -inf gets the K lowest ids and w = 0.  NaN counts as
+ * -inf and +inf as the largest finite fp32; both set EP_DEV_BAD_LOGIT.
+ * logits, topk_ids, w and bias need the alignment of their element type only.
+ * EP_ERR_ARG: a bad shape or type, E % n_group, n_group > 32, topk_group outside
+ * [1, n_group] or holding fewer than K experts, group_top other than 1 or 2.
+ */
+EP_API int ep_router(const void* logits, int dtype, int64_t T, int E, int64_t ld, int K, int score,
+                     const float* bias, int n_group, int topk_group, int group_top, int renorm, float scale,
+                     int32_t* topk_ids, float* w, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Backward of ep_router: the gradient of w (ep_combine_backward's dw) to that of
+ * the logits; topk_ids are constants, and the bias has no gradient.
+ *   dw       [T, K] fp32; logits and topk_ids as ep_router took and gave them.
+ *   dlogits  [T, E] out, of the logits' type, row t at t*ld_out elements; every
+ *            element is written.  fp32 inside, one rounding.
+ * An expert that stands twice among a token's ids gets the sum of its terms; an
+ * id outside [0, E) takes no part and sets EP_DEV_BAD_EXPERT_ID.
+ */
+EP_API int ep_router_backward(const float* dw, const void* logits, int dtype, int64_t T, int E, int64_t ld,
+                              const int32_t* topk_ids, int K, int score, int renorm, float scale, void* dlogits,
+                              int64_t ld_out, int32_t* dev_status, cudaStream_t stream);
 
 /*
  * Self-test of failure detection (no counterpart on the pages): runs

@@ -1,0 +1,426 @@
+"""The router and its gradient (-m gpu) against the definition in 64 bits: which
+experts, in which order, and the weights within the bounds of their fp32 steps."""
+import ctypes
+
+import numpy as np
+import pytest
+
+gpu = pytest.mark.gpu
+
+
+def ref_router(x, K, score, bias=None, n_group=1, topk_group=1, group_top=1, renorm=True, scale=1.0):
+    """(ids, w) from the definition, token by token, in fp64.  x: fp64 logits."""
+    T, E = x.shape
+    ids, w = np.zeros((T, K), np.int32), np.zeros((T, K))
+    length = E // n_group
+    for t in range(T):
+        s = ref_scores(x[t], score)
+        key = x[t].copy() if bias is None else np.where(np.isinf(x[t]), -np.inf, s + bias)
+        by = s if bias is None and n_group > 1 and group_top == 2 else key
+        by = np.where(np.isinf(x[t]), -np.inf, by)
+        groups = []
+        for g in range(n_group):
+            best = sorted((v for v in by[g * length:(g + 1) * length] if v != -np.inf), reverse=True)[:group_top]
+            groups.append(sum(best) if best else -np.inf)
+        kept = sorted(range(n_group), key=lambda g: (-groups[g], g))[:topk_group]
+        order = sorted((e for e in range(E) if e // length in kept), key=lambda e: (-key[e], e))
+        ids[t] = order[:K]
+        c = s[ids[t]]
+        if renorm:
+            c = ref_ratio(x[t][ids[t]], score)
+        w[t] = scale * c
+    return ids, w
+
+
+def ref_scores(x, score):
+    if score == "sigmoid":
+        return np.array([1 / (1 + np.exp(-v)) if v > -700 else 0.0 for v in x])
+    m = x.max()
+    if m == -np.inf:
+        return np.zeros_like(x)
+    e = np.exp(x - m)
+    return e / e.sum()
+
+
+def ref_ratio(x, score):
+    if np.all(x == -np.inf):
+        return np.zeros_like(x)
+    # logs of the scores, so that scores far below the smallest double still have their ratio
+    log = x if score == "softmax" else -np.logaddexp(0.0, -x)
+    e = np.exp(log - log.max())
+    return e / e.sum()
+
+
+def w_bound(x, want, ids, scale):
+    """|w - want| of the fp32 steps: exp(x - m) is off by |x - m| half-units (the rounded difference) and two units of
+    its own; sum, quotient and scale add a few more; the smallest results are subnormal."""
+    chosen = np.take_along_axis(x, ids.astype(np.int64), 1)
+    top = np.max(x, 1, keepdims=True)
+    far = np.where(np.isfinite(chosen) & np.isfinite(top), np.abs(chosen - top), 0.0)
+    return (far + 16) * 2.0 ** -23 * np.abs(want) + abs(scale) * 2.0 ** -140
+
+
+def logits_of(T, E, dtype, seed, spread=1.0, masked=0.0):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    x = spread * (torch.randn((T, E), generator=g) + torch.randn(E, generator=g))
+    if masked:
+        x[torch.rand((T, E), generator=g) < masked] = -float("inf")
+        if T > 3:
+            x[3] = -float("inf")      # a row whose mask leaves nothing
+            x[2, :-1] = -float("inf")  # and one that it leaves one expert
+    return x.to(dtype)
+
+
+def call(x, K, dtype_w=None, **kw):
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    T = x.shape[0]
+    ids = torch.full((T, K), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, K), 77.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    b = kw.pop("bias", None)
+    tdh.ep_router(x, ids, w, bias=None if b is None else torch.from_numpy(b.astype(np.float32)).cuda(), dev_status=st,
+                  **kw)
+    return ids.cpu().numpy(), w.cpu().numpy().astype(np.float64), tdh.ep_status_read(st)
+
+
+CASES = [  # T, E, K, score, bias scale, n_group, topk_group, group_top, renorm, scale
+    (1, 1, 1, "softmax", None, 1, 1, 1, True, 1.0),
+    (1, 256, 8, "sigmoid", 0.1, 8, 4, 2, True, 2.5),
+    (65, 64, 6, "softmax", None, 1, 1, 1, False, 1.0),
+    (65, 64, 6, "softmax", None, 1, 1, 1, True, 1.0),
+    (40, 384, 8, "sigmoid", 0.1, 1, 1, 1, True, 1.0),
+    (33, 17, 17, "sigmoid", None, 1, 1, 1, False, 0.5),
+    (33, 33, 32, "softmax", 0.01, 1, 1, 1, False, 1.0),
+    (20, 1024, 8, "softmax", 0.01, 32, 5, 2, True, 1.0),
+    (20, 1000, 7, "sigmoid", None, 8, 3, 2, True, 1.0),
+    (20, 1000, 7, "softmax", None, 8, 3, 1, False, 1.0),
+    (20, 160, 6, "softmax", None, 8, 3, 1, False, 16.0),
+    (31, 16, 2, "softmax", None, 16, 2, 2, True, 1.0),
+    (9, 72, 32, "sigmoid", 0.1, 2, 2, 1, True, 1.0),
+    (9, 100, 3, "sigmoid", 1.0, 5, 1, 2, True, 1.0),
+    (700, 128, 4, "softmax", None, 1, 1, 1, True, 1.0),
+    (50, 40, 1, "sigmoid", 0.1, 1, 1, 1, True, 1.0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "_".join(str(v) for v in c))
+def test_router_matches_the_definition(case, masked, dtype):
+    import torch
+    T, E, K, score, b, ng, tg, gt, renorm, scale = case
+    x = logits_of(T, E, getattr(torch, dtype), T + E + K, masked=masked)
+    bias = None if b is None else (b * np.random.default_rng(E).standard_normal(E)).astype(np.float32)
+    kw = dict(score=score, n_group=ng, topk_group=tg, group_top=gt, renorm=renorm, scale=scale)
+    ids, w, st = call(x.cuda(), K, bias=bias, **kw)
+    x64 = x.double().numpy()
+    want_ids, want = ref_router(x64, K, bias=None if bias is None else bias.astype(np.float64), **kw)
+    assert st == 0
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(x64, want, ids, scale))
+
+
+@gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+@pytest.mark.parametrize("bias", [None, 0.0, 0.25])
+def test_experts_closer_than_32_bit_scores_tell_apart(score, groups, bias):
+    """Neighbouring fp32 logits: the scores differ by less than an fp32 score's last place, and equal logits tie."""
+    import torch
+    T, E, K = 64, 64, 8
+    rng = np.random.default_rng(5)
+    base = rng.choice([0.5, 2.0, -3.0], size=(T, 1)).astype(np.float32)
+    step = rng.choice([0, 1, 3, 9, 27], size=(T, E))  # no two different pairs have the same sum
+    x = base.copy().repeat(E, 1)
+    for i in range(27):
+        x = np.where(step > i, np.nextafter(x, np.float32(np.inf)), x)
+    b = None if bias is None else np.full(E, bias, np.float32)
+    kw = dict(score=score, n_group=groups[0], topk_group=groups[1], group_top=groups[2])
+    ids, w, st = call(torch.from_numpy(x).cuda(), K, bias=b, **kw)
+    want_ids, want = ref_router(x.astype(np.float64), K, bias=None if b is None else b.astype(np.float64), **kw)
+    assert st == 0
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(x.astype(np.float64), want, ids, 1.0))
+
+
+@gpu
+@pytest.mark.parametrize("E,K", [(64, 8), (96, 32), (1024, 5)])
+@pytest.mark.parametrize("what", ["equal", "lowest", "two values"])
+def test_ties_go_to_the_lower_index(E, K, what):
+    import torch
+    x = torch.zeros((5, E))
+    if what == "lowest":
+        x += torch.finfo(torch.float32).min
+    if what == "two values":
+        x[:, 1::2] = 1.0
+    ids, w, st = call(x.cuda(), K, score="softmax")
+    want = np.arange(K) if what != "two values" else np.concatenate([np.arange(1, E, 2), np.arange(0, E, 2)])[:K]
+    assert st == 0
+    np.testing.assert_array_equal(ids, np.tile(want, (5, 1)))
+    ones = np.array([1.0 if what != "two values" or e % 2 else np.exp(-1.0) for e in want])
+    np.testing.assert_allclose(w, np.tile(ones / ones.sum(), (5, 1)), rtol=20 * 2.0 ** -23)
+
+
+@gpu
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_far_logits_keep_their_ratios(score, renorm):
+    import torch
+    x = torch.tensor([[-300.0, -301.0, -302.5, -299.0], [300.0, 299.0, 250.0, -300.0], [-95.0, -96.0, -97.0, -120.0],
+                      [torch.finfo(torch.float32).min] * 3 + [0.0], [88.0, 30.0, 17.0, 16.0]])
+    ids, w, st = call(x.cuda(), 3, score=score, renorm=renorm)
+    want_ids, want = ref_router(x.double().numpy(), 3, score, renorm=renorm)
+    assert st == 0
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(x.double().numpy(), want, ids, 1.0))
+
+
+@gpu
+def test_nan_and_infinite_logits_are_flagged_and_defined():
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    x = logits_of(6, 20, torch.float32, 3)
+    x[1, 4] = float("nan")
+    x[2, 7] = float("inf")
+    x[4] = float("nan")
+    ids, w, st = call(x.cuda(), 4, score="softmax", renorm=False)
+    assert st == tdh.EP_DEV_BAD_LOGIT
+    y = torch.nan_to_num(x, nan=-float("inf"), posinf=torch.finfo(torch.float32).max, neginf=-float("inf"))
+    want_ids, want = ref_router(y.double().numpy(), 4, "softmax", renorm=False)
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(y.double().numpy(), want, ids, 1.0))
+    assert ids[2, 0] == 7 and w[2, 0] == 1.0 and list(ids[4]) == [0, 1, 2, 3] and np.all(w[4] == 0)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_rows_of_a_wider_matrix(dtype):
+    """Any row stride and any start: the logits as columns of a wider projection, outputs into slices."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    T, E, K = 50, 64, 6
+    wide = logits_of(T, 131, getattr(torch, dtype), 9).cuda()
+    for off in (0, 1, 3, 64):
+        x = wide[:, off:off + E]
+        ids = torch.full((T + 2, K), -7, dtype=torch.int32, device="cuda")
+        w = torch.full((T + 2, K), 77.0, device="cuda")
+        tdh.ep_router(x, ids[1:T + 1], w[1:T + 1], score="sigmoid")
+        want_ids, want = ref_router(x.double().cpu().numpy(), K, "sigmoid")
+        np.testing.assert_array_equal(ids[1:T + 1].cpu().numpy(), want_ids)
+        assert np.all(np.abs(w[1:T + 1].cpu().numpy() - want) <= w_bound(x.double().cpu().numpy(), want, want_ids, 1.0))
+        assert torch.all(ids[[0, T + 1]] == -7) and torch.all(w[[0, T + 1]] == 77.0)
+        out = torch.full((T, 131), 5.0, dtype=wide.dtype, device="cuda")
+        dw = torch.randn((T, K), device="cuda")
+        tdh.ep_router_backward(dw, x, ids[1:T + 1], out[:, off:off + E], score="softmax", renorm=False)
+        want, mag = ref_backward(dw.double().cpu().numpy(), x.double().cpu().numpy(), want_ids, "softmax", False, 1.0)
+        check_backward(out[:, off:off + E], want, mag, x)
+        assert torch.all(out[:, :off] == 5.0) and torch.all(out[:, off + E:] == 5.0)
+
+
+# ------------------------------------------------------------------ backward
+
+def ref_backward(dw, x, ids, score, renorm, scale):
+    """(dlogits, sum of the magnitudes of its terms) from the Jacobian of the definition, in fp64."""
+    T, E = x.shape
+    out, mag = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        ok = (ids[t] >= 0) & (ids[t] < E)
+        j, d = ids[t][ok], scale * dw[t][ok]
+        s = ref_scores(x[t], score)
+        if renorm:
+            r = ref_ratio(x[t][j], score)
+            slope = 1 - s[j] if score == "sigmoid" else 1.0
+            inner, absinner = (d * r).sum(), np.abs(d * r).sum()
+            np.add.at(out[t], j, r * slope * (d - inner))
+            np.add.at(mag[t], j, r * slope * (np.abs(d) + absinner))
+        elif score == "sigmoid":
+            np.add.at(out[t], j, d * s[j] * (1 - s[j]))
+            np.add.at(mag[t], j, np.abs(d) * s[j] * (1 - s[j]))
+        else:
+            out[t] -= s * (d * s[j]).sum()
+            mag[t] += s * np.abs(d * s[j]).sum()
+            np.add.at(out[t], j, d * s[j])
+            np.add.at(mag[t], j, np.abs(d) * s[j])
+    return out, mag
+
+
+def check_backward(got, want, mag, x):
+    """fp32 steps: each term within (range + 32) units of 2^-23 of its magnitude (exp of rounded differences, sums over
+    at most 1024 scores by 32 lanes); then one rounding to the output's type."""
+    import torch
+    xs = x.double().cpu().numpy()
+    fin = np.where(np.isfinite(xs), xs, 0.0)
+    far = min(120.0, float(fin.max() - fin.min())) if fin.size else 0.0
+    half, tiny = torch.finfo(got.dtype).eps / 2, torch.finfo(got.dtype).smallest_normal
+    if got.dtype == torch.float16:
+        tiny *= 2.0 ** -10  # its subnormals
+    bound = (far + 32) * 2.0 ** -23 * mag
+    bound = bound + (np.abs(want) + bound) * half + tiny
+    assert np.all(np.abs(got.double().cpu().numpy() - want) <= bound)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("T,E,K", [(1, 1, 1), (1, 256, 8), (65, 64, 6), (33, 17, 17), (9, 1024, 32), (200, 384, 8),
+                                   (21, 100, 5)])
+def test_backward_matches_the_jacobian(T, E, K, score, renorm, masked, dtype):
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    x = logits_of(T, E, getattr(torch, dtype), T + E, spread=2.0, masked=masked)
+    ids, _, _ = call(x.cuda(), K, score=score)
+    dw = torch.randn((T, K), generator=torch.Generator().manual_seed(K))
+    out = torch.full((T, E), float("nan"), dtype=x.dtype, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tdh.ep_router_backward(dw.cuda(), x.cuda(), torch.from_numpy(ids).cuda(), out, score=score, renorm=renorm, scale=1.5,
+                           dev_status=st)
+    assert tdh.ep_status_read(st) == 0
+    want, mag = ref_backward(dw.double().numpy(), x.double().numpy(), ids, score, renorm, 1.5)
+    check_backward(out, want, mag, x)
+
+
+@gpu
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_backward_matches_differences_of_the_forward(score, renorm):
+    """Central differences of the definition (fp64 on the host) at the experts that were chosen."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    T, E, K = 6, 24, 4
+    x = logits_of(T, E, torch.float32, 4)
+    ids, _, _ = call(x.cuda(), K, score=score)
+    dw = np.random.default_rng(2).standard_normal((T, K)).astype(np.float32)
+    out = torch.empty((T, E), device="cuda")
+    tdh.ep_router_backward(torch.from_numpy(dw).cuda(), x.cuda(), torch.from_numpy(ids).cuda(), out, score=score,
+                           renorm=renorm)
+
+    def loss(v):
+        w = np.array([ref_ratio(v[t][ids[t]], score) if renorm else ref_scores(v[t], score)[ids[t]] for t in range(T)])
+        return (w * dw).sum(1)
+
+    x64, eps = x.double().numpy(), 1e-5
+    for e in range(E):
+        hi, lo = x64.copy(), x64.copy()
+        hi[:, e] += eps
+        lo[:, e] -= eps
+        # the difference quotient is off by eps^2 times a third derivative below 1
+        np.testing.assert_allclose(out[:, e].cpu().numpy(), (loss(hi) - loss(lo)) / (2 * eps), atol=2e-6)
+
+
+@gpu
+def test_backward_of_repeated_and_bad_ids():
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    T, E, K = 4, 12, 5
+    x = logits_of(T, E, torch.float32, 8)
+    ids = np.array([[3, 3, 3, 1, 0], [2, 5, 2, 5, 2], [0, 12, -1, 4, 7], [-1, -1, 99, -5, 1 << 30]], np.int32)
+    dw = torch.randn((T, K), generator=torch.Generator().manual_seed(1))
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            out = torch.full((T, E), float("nan"), device="cuda")
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            tdh.ep_router_backward(dw.cuda(), x.cuda(), torch.from_numpy(ids).cuda(), out, score=score, renorm=renorm,
+                                   dev_status=st)
+            assert tdh.ep_status_read(st) == tdh.EP_DEV_BAD_EXPERT_ID
+            want, mag = ref_backward(dw.double().numpy(), x.double().numpy(), ids, score, renorm, 1.0)
+            check_backward(out, want, mag, x)
+
+
+@gpu
+def test_zero_tokens_and_another_stream_and_a_graph():
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    e = torch.empty((0, 64), device="cuda")
+    tdh.ep_router(e, torch.empty((0, 4), dtype=torch.int32, device="cuda"), torch.empty((0, 4), device="cuda"))
+    tdh.ep_router_backward(torch.empty((0, 4), device="cuda"), e, torch.empty((0, 4), dtype=torch.int32, device="cuda"),
+                           torch.empty((0, 64), device="cuda"))
+    T, E, K = 300, 64, 6
+    x = logits_of(T, E, torch.float32, 1).cuda()
+    ids = torch.zeros((T, K), dtype=torch.int32, device="cuda")
+    w = torch.zeros((T, K), device="cuda")
+    dx = torch.zeros((T, E), device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    tdh.ep_router(x, ids, w, score="sigmoid", stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    first = (ids.clone(), w.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tdh.ep_router(x, ids, w, score="sigmoid")
+        tdh.ep_router_backward(w, x, ids, dx, score="sigmoid")
+    x.copy_(logits_of(T, E, torch.float32, 2))
+    graph.replay()
+    want_ids, want = ref_router(x.double().cpu().numpy(), K, "sigmoid")
+    np.testing.assert_array_equal(ids.cpu().numpy(), want_ids)
+    assert not torch.equal(ids, first[0])
+    d, mag = ref_backward(w.double().cpu().numpy(), x.double().cpu().numpy(), want_ids, "sigmoid", True, 1.0)
+    check_backward(dx, d, mag, x)
+
+
+# ------------------------------------------------------------------ refusals (no GPU needed)
+
+def test_router_argument_errors():
+    import token_dispatch_histogram_b200 as tdh
+    L = tdh.lib()
+    fake, odd = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1001)
+
+    def fwd(logits=fake, dtype=0, T=4, E=16, ld=16, K=2, score=0, bias=None, ng=1, tg=1, gt=1, scale=1.0, ids=fake,
+            w=fake):
+        return L.ep_router(logits, dtype, T, E, ld, K, score, bias, ng, tg, gt, 1, scale, ids, w, None, None)
+
+    bad = [dict(dtype=3), dict(dtype=-1), dict(T=-1), dict(E=0), dict(E=1025, ld=1025), dict(ld=15), dict(K=0),
+           dict(K=17), dict(E=64, ld=64, K=33), dict(score=2), dict(ng=0), dict(ng=3), dict(E=33, ld=33, ng=33, tg=33),
+           dict(ng=4, tg=0), dict(ng=4, tg=5), dict(ng=16, tg=1), dict(gt=0), dict(gt=3), dict(scale=float("nan")),
+           dict(scale=float("inf")), dict(logits=None), dict(ids=None), dict(w=None), dict(logits=odd), dict(ids=odd),
+           dict(w=odd), dict(bias=odd), dict(T=1 << 31, K=2)]
+    for kw in bad:
+        assert fwd(**kw) == tdh.EP_ERR_ARG, kw
+    assert fwd(T=0, logits=None, ids=None, w=None) == tdh.EP_OK
+
+    def bwd(dw=fake, logits=fake, dtype=0, T=4, E=16, ld=16, ids=fake, K=2, score=0, scale=1.0, out=fake, ldo=16):
+        return L.ep_router_backward(dw, logits, dtype, T, E, ld, ids, K, score, 1, scale, out, ldo, None, None)
+
+    for kw in [dict(dtype=3), dict(T=-1), dict(ld=15), dict(ldo=15), dict(K=17), dict(score=5), dict(dw=None),
+               dict(ids=None), dict(out=None), dict(logits=None), dict(out=odd), dict(dw=odd), dict(scale=float("nan"))]:
+        assert bwd(**kw) == tdh.EP_ERR_ARG, kw
+    assert bwd(T=0, dw=None, logits=None, ids=None, out=None) == tdh.EP_OK
+
+
+def test_router_binding_refuses_wrong_tensors():
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    x, ids, w = torch.zeros(4, 16), torch.zeros((4, 2), dtype=torch.int32), torch.zeros(4, 2)
+    with pytest.raises(ValueError):
+        tdh.ep_router(x, ids, w)  # CPU tensors
+    with pytest.raises(TypeError):
+        tdh.ep_router(x.double(), ids, w)
+    with pytest.raises(TypeError):
+        tdh.ep_router(x, ids.long(), w)
+    with pytest.raises(TypeError):
+        tdh.ep_router(x, ids, w.half())
+    with pytest.raises(ValueError):
+        tdh.ep_router(x, ids, w, score="tanh")
+    with pytest.raises(ValueError):
+        tdh.ep_router(x.T, ids, w)
+
+
+@gpu
+def test_router_binding_refuses_wrong_shapes():
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    x = torch.zeros((4, 16), device="cuda")
+    ids, w = torch.zeros((4, 2), dtype=torch.int32, device="cuda"), torch.zeros((4, 2), device="cuda")
+    with pytest.raises(ValueError):
+        tdh.ep_router(x, ids[:3], w)
+    with pytest.raises(ValueError):
+        tdh.ep_router(x, ids, w[:, :1])
+    with pytest.raises(ValueError):
+        tdh.ep_router(x, ids, w, bias=torch.zeros(15, device="cuda"))
+    with pytest.raises(tdh.EpError):
+        tdh.ep_router(x[:1].expand(4, 16), ids, w)  # rows on top of each other
+    with pytest.raises(tdh.EpError):
+        tdh.ep_router(x, ids, w, n_group=3, topk_group=1)
+    with pytest.raises(TypeError):
+        tdh.ep_router_backward(w, x, ids, torch.zeros((4, 16), dtype=torch.bfloat16, device="cuda"))

@@ -8,6 +8,7 @@ If libep.so is missing the import fails.
 
 Device memory and streams come from PyTorch; nothing here computes.
 """
+import contextlib
 import ctypes
 import os
 
@@ -22,9 +23,11 @@ EP_DEV_LOOKBACK_TIMEOUT = 0x2
 EP_DEV_BAD_LOADS = 0x4
 EP_DEV_BAD_ROW = 0x8
 EP_DEV_COPY_TIMEOUT = 0x10
+EP_DEV_BAD_LOGIT = 0x20
 EP_MAX_EXPERTS = 1024
 EP_MAX_RANKS = 1024
-EP_DTYPE_F32, EP_DTYPE_BF16 = 0, 1
+EP_DTYPE_F32, EP_DTYPE_BF16, EP_DTYPE_F16 = 0, 1, 2
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_IPC_HANDLE_BYTES = 64
 
 
@@ -55,6 +58,7 @@ class EpQuotaLayout(ctypes.Structure):
 
 _lib = None
 _V, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_F, _D = ctypes.c_float, ctypes.c_double
 
 _SIGS = {
     "ep_version": (ctypes.c_char_p, []),
@@ -93,6 +97,8 @@ _SIGS = {
     "ep_ipc_export": (_I, [_V, _V, _V]),
     "ep_ipc_open": (_I, [_V, ctypes.c_uint64, _V, _V]),
     "ep_ipc_close": (_I, [_V]),
+    "ep_router": (_I, [_V, _I, _I64, _I, _I64, _I, _I, _V, _I, _I, _I, _I, _F, _V, _V, _V, _V]),
+    "ep_router_backward": (_I, [_V, _V, _I, _I64, _I, _I64, _V, _I, _I, _I, _F, _V, _I64, _V, _V]),
     "ep_status_read": (_I, [_V, _V, _V]),
     "ep_selftest_lookback_timeout": (_I, [_V, _I64, _I, _I, _V, _V, _V, _SZ, _V, _V]),
 }
@@ -141,6 +147,37 @@ def _s(stream):
 def _dtype(t, *dts):
     if t.dtype not in dts:
         raise TypeError(f"dtype {t.dtype}, expected one of {dts}")
+
+
+def _rows(t):
+    """Pointer of a 2-d tensor whose rows are contiguous, at any row stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a 2-d tensor with contiguous rows")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _ld(t):
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _shape(what, t, *shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+
+
+@contextlib.contextmanager
+def _device_of(first, *others):
+    """The tensors' device current (they must share one), whatever the caller's
+    current device is."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if not first.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    with torch.cuda.device(first.device):
+        yield
 
 
 def version():
@@ -506,6 +543,54 @@ def ep_quota_replica_grad_reduce_peer(g_home_local, peers, rep_rows, rep_dtype, 
            lib().ep_quota_replica_grad_reduce_peer(_p(g_home_local), _p(peers), rep_rows, dt, n, E, peers.numel(), rank,
                                                    _p(plan), plan.numel(), int(bool(clear_replicas)), _p(dev_status),
                                                    _s(stream)))
+
+
+_LOGIT_DTYPES = {torch.float32: EP_DTYPE_F32, torch.bfloat16: EP_DTYPE_BF16, torch.float16: EP_DTYPE_F16}
+_SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+
+
+def _router_args(logits, topk_ids, w, score):
+    _dtype(logits, *_LOGIT_DTYPES)
+    _dtype(topk_ids, torch.int32)
+    _dtype(w, torch.float32)
+    if score not in _SCORES:
+        raise ValueError(f"score {score!r}, expected one of {sorted(_SCORES)}")
+    _rows(logits)
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    _shape("topk_ids", topk_ids, T, K)
+    _shape("gate weights", w, T, K)
+    return T, E, K, _LOGIT_DTYPES[logits.dtype], _SCORES[score]
+
+
+def ep_router(logits, topk_ids, w, score="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renorm=True,
+              scale=1.0, dev_status=None, stream=None):
+    """The K experts of each token and their gate weights from router logits
+    [T, E] (fp32, bf16 or fp16, any row stride); K = topk_ids.shape[1].  score:
+    "softmax" or "sigmoid"; bias [E] moves the choice only; of the n_group
+    groups only the topk_group best are taken from (see ep.h)."""
+    T, E, K, dt, sc = _router_args(logits, topk_ids, w, score)
+    if bias is not None:
+        _dtype(bias, torch.float32)
+        _shape("bias", bias, E)
+    with _device_of(logits, topk_ids, w, bias, dev_status):
+        _check("ep_router", lib().ep_router(_rows(logits), dt, T, E, _ld(logits), K, sc, _p(bias), n_group,
+                                            topk_group, group_top, int(bool(renorm)), scale, _p(topk_ids), _p(w),
+                                            _p(dev_status), _s(stream)))
+
+
+def ep_router_backward(dw, logits, topk_ids, dlogits, score="softmax", renorm=True, scale=1.0, dev_status=None,
+                       stream=None):
+    """dlogits [T, E] from the gradient dw [T, K] of the gate weights; score,
+    renorm and scale as ep_router had them."""
+    T, E, K, dt, sc = _router_args(logits, topk_ids, dw, score)
+    _dtype(dlogits, logits.dtype)
+    _shape("dlogits", dlogits, T, E)
+    with _device_of(logits, dw, topk_ids, dlogits, dev_status):
+        _check("ep_router_backward",
+               lib().ep_router_backward(_p(dw), _rows(logits), dt, T, E, _ld(logits), _p(topk_ids), K, sc,
+                                        int(bool(renorm)), scale, _rows(dlogits), _ld(dlogits), _p(dev_status),
+                                        _s(stream)))
 
 
 def ep_selftest_lookback_timeout(topk_ids, E, loads, max_vio, ws, dev_status, stream=None):

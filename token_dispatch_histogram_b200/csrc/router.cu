@@ -1,0 +1,365 @@
+// The router in front of the dispatch path: router logits to the K experts of
+// each token and their gate weights, and the gradient of the weights.
+//
+// With x the logits of one token, s = softmax(x) or sigmoid(x) element by
+// element, and b an optional bias per expert that balances the loads:
+//   key_e = s_e + b_e, or x_e without a bias (the same order as s_e)
+//   groups: the experts fall into n_group runs of E / n_group; a group's score
+//     is its best key, or the sum of its best two (s_e without a bias); only
+//     experts of the topk_group best groups are taken
+//   ids = the K largest keys, descending; equal ones (of experts or of groups)
+//     by ascending index
+//   w_k = scale * s_k, or with renorm scale * s_k / sum_j s_j
+// The bias moves the choice only; the weights and their gradient do not see it.
+//
+// Which of two experts comes first is decided by numbers that can lie closer
+// than 32-bit scores tell apart, so keys and group scores are held in 64 bits.
+// The weights are 32-bit: each is a ratio of exponentials of differences of the
+// chosen logits, exact to a few units in the last place at any magnitude.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <float.h>
+#include <math.h>
+
+#include "common.cuh"
+
+namespace ep {
+
+constexpr int ROUTER_WARPS = 8;
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// A logit as the definitions take it: -inf masks an expert, NaN counts as -inf
+// and +inf as the largest finite value (both are flagged), so that every output
+// is defined.
+__device__ __forceinline__ float clean_logit(float x, bool& bad) {
+  if (x <= FLT_MAX) return x;  // false for NaN and +inf
+  bad = true;
+  return x > 0.f ? FLT_MAX : -INFINITY;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// s / sum_j s_j of the chosen logits (lane k < K holds x_k, the others -inf),
+// 0 in a row whose chosen logits are all -inf.  Both scores are e^x / (1 + e^x)
+// or e^x over a common factor, so the ratio is taken of numbers scaled by the
+// largest: no sum under- or overflows.
+__device__ __forceinline__ float chosen_ratio(float x, bool sigmoid) {
+  const float m = warp_max(x);
+  if (m == -INFINITY) return 0.f;
+  float t;
+  if (!sigmoid)
+    t = expf(x - m);
+  else if (x >= 0.f)
+    t = 1.f / (1.f + expf(-x));
+  else
+    t = expf(x - fminf(m, 0.f)) / (1.f + expf(x));
+  return t / warp_sum(t);
+}
+
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  if (x >= 0.f) return 1.f / (1.f + expf(-x));
+  const float e = expf(x);
+  return e / (1.f + e);
+}
+
+struct RouterArgs {
+  int64_t T, ld;
+  int E, K, n_group, topk_group, group_top;
+  bool sigmoid, renorm;
+  float scale;
+};
+
+// One token by one warp, everything that decides held in 64 bits; key: E doubles
+// of the warp's own.  Lane k < K returns the k-th expert.
+template <typename V>
+__device__ int select_exact(const RouterArgs& a, const V* __restrict__ row, const float* __restrict__ bias,
+                            double* key) {
+  const int lane = threadIdx.x & 31;
+  const int len = a.E / a.n_group;
+  const bool scores = bias != nullptr || (a.n_group > 1 && a.group_top == 2);
+  bool bad = false;
+  double m = -INFINITY, z = 0.0;
+  if (scores && !a.sigmoid) {
+    float mx = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) mx = fmaxf(mx, clean_logit(to_f32(row[e]), bad));
+    m = warp_max(mx);
+    for (int e = lane; e < a.E; e += 32) {
+      const float x = clean_logit(to_f32(row[e]), bad);
+      if (x != -INFINITY) z += exp((double)x - m);
+    }
+    z = warp_sum(z);
+  }
+  for (int e = lane; e < a.E; e += 32) {
+    const double x = clean_logit(to_f32(row[e]), bad);
+    double k = x;
+    if (scores && x != -INFINITY) {
+      if (!a.sigmoid)
+        k = exp(x - m) / z;
+      else if (x >= 0.0)
+        k = 1.0 / (1.0 + exp(-x));
+      else
+        k = exp(x) / (1.0 + exp(x));
+      if (bias) k += (double)bias[e];
+    }
+    key[e] = k;
+  }
+  __syncwarp();
+  uint32_t keep = 0xffffffffu;
+  if (a.n_group > 1) {
+    // lane g: the score of group g over its experts that are not masked
+    double first = -INFINITY, second = -INFINITY;
+    if (lane < a.n_group)
+      for (int i = 0; i < len; ++i) {
+        const double k = key[lane * len + i];
+        if (k > first) {
+          second = first;
+          first = k;
+        } else if (k > second) {
+          second = k;
+        }
+      }
+    double score = first;
+    if (a.group_top == 2 && second != -INFINITY) score += second;
+    int before = 0;
+    for (int g = 0; g < a.n_group; ++g) {
+      const double o = __shfl_sync(0xffffffffu, score, g);
+      before += o > score || (o == score && g < lane);
+    }
+    keep = __ballot_sync(0xffffffffu, lane < a.n_group && before < a.topk_group);
+    if (!bias && a.group_top == 2) {  // the groups were chosen by scores, the experts are by logits
+      __syncwarp();
+      for (int e = lane; e < a.E; e += 32) key[e] = clean_logit(to_f32(row[e]), bad);
+      __syncwarp();
+    }
+  }
+  int mine = 0;
+  for (int k = 0; k < a.K; ++k) {
+    double best = 0.0;
+    int at = INT_MAX;
+    for (int e = lane; e < a.E; e += 32) {
+      const double v = key[e];
+      if (isnan(v) || !(keep >> (a.n_group > 1 ? e / len : 0) & 1)) continue;  // taken, or of a group left out
+      if (at == INT_MAX || v > best) {
+        best = v;
+        at = e;
+      }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const double v = __shfl_xor_sync(0xffffffffu, best, d);
+      const int o = __shfl_xor_sync(0xffffffffu, at, d);
+      if (o != INT_MAX && (at == INT_MAX || v > best || (v == best && o < at))) {
+        best = v;
+        at = o;
+      }
+    }
+    if (lane == k) mine = at;
+    if (lane == (at & 31)) key[at] = NAN;
+    __syncwarp();
+  }
+  return mine;
+}
+
+template <typename V>
+__global__ void __launch_bounds__(ROUTER_WARPS * 32)
+    k_router(const V* __restrict__ logits, const float* __restrict__ bias, RouterArgs a, int32_t* __restrict__ ids,
+             float* __restrict__ w, int32_t* dev_status) {
+  extern __shared__ double s_key[];  // [warps][E]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + warp;
+  if (t >= a.T) return;
+  const V* row = logits + t * a.ld;
+  bool bad = false;
+  for (int e = lane; e < a.E; e += 32) clean_logit(to_f32(row[e]), bad);
+  const int id = select_exact(a, row, bias, s_key + (size_t)warp * a.E);
+  bool ignore = false;
+  const float x = lane < a.K ? clean_logit(to_f32(row[id]), ignore) : -INFINITY;
+  float v;
+  if (a.renorm) {
+    v = chosen_ratio(x, a.sigmoid);
+  } else if (a.sigmoid) {
+    v = sigmoid_f32(x);
+  } else {
+    float m = -INFINITY, z = 0.f;
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, clean_logit(to_f32(row[e]), ignore));
+    m = warp_max(m);
+    if (m == -INFINITY) {
+      v = 0.f;
+    } else {
+      for (int e = lane; e < a.E; e += 32) z += expf(clean_logit(to_f32(row[e]), ignore) - m);
+      v = expf(x - m) / warp_sum(z);
+    }
+  }
+  if (lane < a.K) {
+    ids[t * a.K + lane] = id;
+    w[t * a.K + lane] = a.scale * v;
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) flag(dev_status, EP_DEV_BAD_LOGIT);
+}
+
+// The gradient of the weights: dlogits of one token by one warp, its row built
+// in shared memory and written once.  With r_k = s_k / sum_j s_j:
+//   softmax, renorm   dx_k = scale r_k (dw_k - i),            i = sum_j dw_j r_j
+//   sigmoid, renorm   dx_k = scale r_k (1 - s_k) (dw_k - i)
+//   sigmoid           dx_k = scale s_k (1 - s_k) dw_k
+//   softmax           dx_e = scale s_e ([e chosen] dw_e - i), i = sum_j dw_j s_j
+// Only the last touches experts that were not chosen (and has to read the row).
+// An expert that stands twice among a token's ids gets the sum of its terms.
+template <typename V>
+__global__ void __launch_bounds__(ROUTER_WARPS * 32)
+    k_router_backward(const float* __restrict__ dw, const V* __restrict__ logits, const int32_t* __restrict__ ids,
+                      RouterArgs a, int64_t ld_out, V* __restrict__ dlogits, int32_t* dev_status) {
+  extern __shared__ float s_row[];  // [warps][E]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + warp;
+  if (t >= a.T) return;
+  const V* row = logits + t * a.ld;
+  float* out = s_row + (size_t)warp * a.E;
+  bool bad = false;
+  int id = -1;
+  float x = -INFINITY, d = 0.f;
+  bool bad_id = false;
+  if (lane < a.K) {
+    id = ids[t * a.K + lane];
+    bad_id = id < 0 || id >= a.E;
+    if (!bad_id) {
+      x = clean_logit(to_f32(row[id]), bad);
+      d = dw[t * a.K + lane];
+    } else {
+      id = -1;
+    }
+  }
+  float v;  // this lane's term of dlogits[id]
+  if (a.sigmoid || a.renorm) {
+    for (int e = lane; e < a.E; e += 32) out[e] = 0.f;
+    if (a.renorm) {
+      const float r = chosen_ratio(x, a.sigmoid);
+      v = r * (d - warp_sum(d * r));
+      if (a.sigmoid) v *= sigmoid_f32(-x);
+    } else {
+      v = d * sigmoid_f32(x) * sigmoid_f32(-x);
+    }
+  } else {
+    float m = -INFINITY, z = 0.f;
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, clean_logit(to_f32(row[e]), bad));
+    m = warp_max(m);
+    const float m0 = m == -INFINITY ? 0.f : m;  // a row of -inf has scores of 0
+    for (int e = lane; e < a.E; e += 32) z += expf(clean_logit(to_f32(row[e]), bad) - m0);
+    z = warp_sum(z);
+    const float iz = z > 0.f ? 1.f / z : 0.f;
+    v = d * (expf(x - m0) * iz);
+    const float i = warp_sum(v);
+    for (int e = lane; e < a.E; e += 32) out[e] = -i * a.scale * (expf(clean_logit(to_f32(row[e]), bad) - m0) * iz);
+  }
+  __syncwarp();
+  v *= a.scale;
+  const uint32_t same = __match_any_sync(0xffffffffu, id);
+  if (__any_sync(0xffffffffu, id >= 0 && (same & (same - 1)))) {  // the same expert twice: one lane adds all, in order
+    float sum = 0.f;
+    for (int j = 0; j < a.K; ++j) {
+      const float o = __shfl_sync(0xffffffffu, v, j);
+      if (same >> j & 1) sum += o;
+    }
+    if (id >= 0 && (same & lanemask_lt()) == 0) out[id] += sum;
+  } else if (id >= 0) {
+    out[id] += v;
+  }
+  __syncwarp();
+  V* to = dlogits + t * ld_out;
+  for (int e = lane; e < a.E; e += 32) to[e] = from_f32<V>(out[e]);
+  const uint32_t bits = (__any_sync(0xffffffffu, bad) ? EP_DEV_BAD_LOGIT : 0) |
+                        (__any_sync(0xffffffffu, bad_id) ? EP_DEV_BAD_EXPERT_ID : 0);
+  if (bits && lane == 0) flag(dev_status, bits);
+}
+
+static bool valid_router(int dtype, int64_t T, int E, int64_t ld, int K, int score, float scale) {
+  if (!valid_tke(T, K, E) || ld < E) return false;
+  if (dtype != EP_DTYPE_F32 && dtype != EP_DTYPE_BF16 && dtype != EP_DTYPE_F16) return false;
+  return (score == EP_SCORE_SOFTMAX || score == EP_SCORE_SIGMOID) && isfinite(scale);
+}
+
+static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+template <typename V>
+static int run_router(const void* logits, const float* bias, const RouterArgs& a, int32_t* ids, float* w,
+                      int32_t* dev_status, cudaStream_t stream) {
+  const size_t smem = (size_t)ROUTER_WARPS * a.E * sizeof(double);
+  if (!raise_smem_limit((const void*)k_router<V>, smem)) return EP_ERR_CUDA;
+  const unsigned grid = (unsigned)((a.T + ROUTER_WARPS - 1) / ROUTER_WARPS);
+  k_router<V><<<grid, ROUTER_WARPS * 32, smem, stream>>>((const V*)logits, bias, a, ids, w, dev_status);
+  count_launch();
+  return launch_status();
+}
+
+template <typename V>
+static int run_router_backward(const float* dw, const void* logits, const int32_t* ids, const RouterArgs& a,
+                               int64_t ld_out, void* dlogits, int32_t* dev_status, cudaStream_t stream) {
+  const size_t smem = (size_t)ROUTER_WARPS * a.E * sizeof(float);
+  if (!raise_smem_limit((const void*)k_router_backward<V>, smem)) return EP_ERR_CUDA;
+  const unsigned grid = (unsigned)((a.T + ROUTER_WARPS - 1) / ROUTER_WARPS);
+  k_router_backward<V>
+      <<<grid, ROUTER_WARPS * 32, smem, stream>>>(dw, (const V*)logits, ids, a, ld_out, (V*)dlogits, dev_status);
+  count_launch();
+  return launch_status();
+}
+
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_router(const void* logits, int dtype, int64_t T, int E, int64_t ld, int K, int score,
+                         const float* bias, int n_group, int topk_group, int group_top, int renorm, float scale,
+                         int32_t* topk_ids, float* w, int32_t* dev_status, cudaStream_t stream) {
+  if (!valid_router(dtype, T, E, ld, K, score, scale)) return EP_ERR_ARG;
+  if (n_group < 1 || n_group > 32 || E % n_group || topk_group < 1 || topk_group > n_group ||
+      (int64_t)topk_group * (E / n_group) < K || (group_top != 1 && group_top != 2))
+    return EP_ERR_ARG;
+  if (T == 0) return EP_OK;
+  if (!logits || !topk_ids || !w || !aligned_to(logits, dtype == EP_DTYPE_F32 ? 4 : 2) || !aligned_to(bias, 4) ||
+      !aligned_to(topk_ids, 4) || !aligned_to(w, 4))
+    return EP_ERR_ARG;
+  const RouterArgs a{T, ld, E, K, topk_group == n_group ? 1 : n_group, topk_group, group_top,
+                     score == EP_SCORE_SIGMOID, renorm != 0, scale};
+  if (dtype == EP_DTYPE_F32) return run_router<float>(logits, bias, a, topk_ids, w, dev_status, stream);
+  if (dtype == EP_DTYPE_BF16) return run_router<__nv_bfloat16>(logits, bias, a, topk_ids, w, dev_status, stream);
+  return run_router<__half>(logits, bias, a, topk_ids, w, dev_status, stream);
+}
+
+extern "C" int ep_router_backward(const float* dw, const void* logits, int dtype, int64_t T, int E, int64_t ld,
+                                  const int32_t* topk_ids, int K, int score, int renorm, float scale, void* dlogits,
+                                  int64_t ld_out, int32_t* dev_status, cudaStream_t stream) {
+  if (!valid_router(dtype, T, E, ld, K, score, scale) || ld_out < E) return EP_ERR_ARG;
+  if (T == 0) return EP_OK;
+  const size_t size = dtype == EP_DTYPE_F32 ? 4 : 2;
+  if (!dw || !logits || !topk_ids || !dlogits || !aligned_to(logits, size) || !aligned_to(dlogits, size) ||
+      !aligned_to(dw, 4) || !aligned_to(topk_ids, 4))
+    return EP_ERR_ARG;
+  const RouterArgs a{T, ld, E, K, 1, 1, 1, score == EP_SCORE_SIGMOID, renorm != 0, scale};
+  if (dtype == EP_DTYPE_F32)
+    return run_router_backward<float>(dw, logits, topk_ids, a, ld_out, dlogits, dev_status, stream);
+  if (dtype == EP_DTYPE_BF16)
+    return run_router_backward<__nv_bfloat16>(dw, logits, topk_ids, a, ld_out, dlogits, dev_status, stream);
+  return run_router_backward<__half>(dw, logits, topk_ids, a, ld_out, dlogits, dev_status, stream);
+}
