@@ -24,6 +24,9 @@
  * and what stands around it in a model:
  *   ep_router, ep_router_backward (router logits to topk_ids and w, and their
  *       gradient)
+ *   ep_expert_up, ep_expert_gemm, ep_expert_up_backward, ep_expert_wgrad (the
+ *       experts' products over the slots of the dispatch buffer, and their
+ *       gradients)
  *
  * Sources, cited by page title and section:
  *  [GR] "MoonEP: πώς η εξισορρόπηση των AI experts αλλάζει την υποδομή των MoE
@@ -668,6 +671,77 @@ EP_API int ep_router(const void* logits, int dtype, int64_t T, int E, int64_t ld
 EP_API int ep_router_backward(const float* dw, const void* logits, int dtype, int64_t T, int E, int64_t ld,
                               const int32_t* topk_ids, int K, int score, int renorm, float scale, void* dlogits,
                               int64_t ld_out, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The experts' products between dispatch and combine.  An expert is a gated
+ * projection, W13 [2I, H] (gate rows, then up rows) and W2 [H, I]:
+ *   gu = x W13^T,  h = silu(g) * u,  y = h W2^T           silu(g) = g / (1 + e^-g)
+ * and backward, from dy:
+ *   dh = dy W2,  dg = dh u (sg + g sg (1 - sg)),  du = dh g sg,  sg = 1 / (1 + e^-g)
+ *   dx = dgu W13,  dW2 = dy^T h,  dW13 = dgu^T x
+ * Each call runs over the slots of a buffer of `rows` rows, as a plan lays them
+ * out: slot s holds rows [cu_seqlens[s], cu_seqlens[s+1]); its id is
+ * slot_order[s] (NULL: s): the home copy of expert id below the number of
+ * experts n_w, replica m at n_w + m, whose expert is rep_expert[m], and -1 for no
+ * slot.  Those are a plan's cu_seqlens, slot_order and rep_expert as they are
+ * (EpPlanLayout, EpQuotaLayout), with n_slots = E + cap, n_w = E, n_rep = cap.
+ * All three are read on the device.
+ *   - rows outside every slot are neither read into a result nor written;
+ *   - bf16 in and out, fp32 sums and activation, one rounding of each result;
+ *   - widths (H, I, K, M, N) are multiples of 8; every base is 16-byte aligned;
+ *   - a slot with cu_seqlens outside [0, rows] or descending is left out and sets
+ *     EP_DEV_BAD_ROW; one with an id past the replicas, or a replica of no
+ *     expert, EP_DEV_BAD_EXPERT_ID; a wait inside the kernel that ran out,
+ *     EP_DEV_COPY_TIMEOUT.
+ */
+
+/*
+ * y[r] = x[r] W^T (w [n_w, N, K]; the second projection), or with transpose_w
+ * y[r] = x[r] W (w [n_w, K, N]; the first projection's backward: K = 2I, N = H).
+ * x [rows, K], y [rows, N] out.
+ */
+EP_API int ep_expert_gemm(const uint16_t* x, int64_t rows, int64_t K, const uint16_t* w, int n_w, int64_t N,
+                          int transpose_w, const int32_t* cu_seqlens, int n_slots, const int32_t* slot_order,
+                          const int32_t* rep_expert, int n_rep, uint16_t* y, int32_t* dev_status,
+                          cudaStream_t stream);
+
+/*
+ * The first projection and its activation in one pass: h [rows, I] out from
+ * x [rows, H] and w [n_w, 2I, H]; gu [rows, 2I] out (NULL: not kept) for the
+ * backward.  h is computed from the products before their rounding.
+ */
+EP_API int ep_expert_up(const uint16_t* x, int64_t rows, int64_t H, const uint16_t* w, int n_w, int64_t I,
+                        const int32_t* cu_seqlens, int n_slots, const int32_t* slot_order, const int32_t* rep_expert,
+                        int n_rep, uint16_t* h, uint16_t* gu, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Backward through the second projection and the activation: dgu [rows, 2I] out
+ * from dy [rows, H], w2 [n_w, H, I] and the kept gu [rows, 2I]; dh is not
+ * rounded in between.  h [rows, I] out (NULL: not wanted) is the activation
+ * again, for dW2.
+ */
+EP_API int ep_expert_up_backward(const uint16_t* dy, int64_t rows, int64_t H, const uint16_t* w2, int n_w, int64_t I,
+                                 const uint16_t* gu, const int32_t* cu_seqlens, int n_slots,
+                                 const int32_t* slot_order, const int32_t* rep_expert, int n_rep, uint16_t* dgu,
+                                 uint16_t* h, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The weights' gradients, slot by slot: g = a_s^T b_s, [M, N] fp32, of a slot's
+ * rows of a [rows, M] and b [rows, N]; into row e of g_home for the home copy of
+ * expert e, row m of g_rep for replica m, as ep_replica_grad_reduce takes them.
+ * A row may be part of a longer one: row i starts at i * ld_home (ld_rep)
+ * elements, so dW13 and dW2 of an expert can lie one after the other.
+ *   rep_dtype   of g_rep, EP_DTYPE_F32 or EP_DTYPE_BF16.
+ *   accumulate  != 0: added to what is there (one fp32 add; bf16 rows rounded
+ *               again); otherwise written, zeros for a slot without rows.
+ * Rows that belong to no slot are left as they are.  ld_home and ld_rep are at
+ * least M * N and keep 16-byte alignment.
+ */
+EP_API int ep_expert_wgrad(const uint16_t* a, const uint16_t* b, int64_t rows, int64_t M, int64_t N,
+                           const int32_t* cu_seqlens, int n_slots, const int32_t* slot_order, float* g_home,
+                           int n_home, int64_t ld_home, void* g_rep, int rep_dtype, int n_rep, int64_t ld_rep,
+                           int accumulate, int32_t* dev_status, cudaStream_t stream);
 
 /*
  * Self-test of failure detection (no counterpart on the pages): runs

@@ -99,6 +99,10 @@ _SIGS = {
     "ep_ipc_close": (_I, [_V]),
     "ep_router": (_I, [_V, _I, _I64, _I, _I64, _I, _I, _V, _I, _I, _I, _I, _F, _V, _V, _V, _V]),
     "ep_router_backward": (_I, [_V, _V, _I, _I64, _I, _I64, _V, _I, _I, _I, _F, _V, _I64, _V, _V]),
+    "ep_expert_gemm": (_I, [_V, _I64, _I64, _V, _I, _I64, _I, _V, _I, _V, _V, _I, _V, _V, _V]),
+    "ep_expert_up": (_I, [_V, _I64, _I64, _V, _I, _I64, _V, _I, _V, _V, _I, _V, _V, _V, _V]),
+    "ep_expert_up_backward": (_I, [_V, _I64, _I64, _V, _I, _I64, _V, _V, _I, _V, _V, _I, _V, _V, _V, _V]),
+    "ep_expert_wgrad": (_I, [_V, _V, _I64, _I64, _I64, _V, _I, _V, _V, _I, _I64, _V, _I, _I, _I64, _I, _V, _V]),
     "ep_status_read": (_I, [_V, _V, _V]),
     "ep_selftest_lookback_timeout": (_I, [_V, _I64, _I, _I, _V, _V, _V, _SZ, _V, _V]),
 }
@@ -591,6 +595,107 @@ def ep_router_backward(dw, logits, topk_ids, dlogits, score="softmax", renorm=Tr
                lib().ep_router_backward(_p(dw), _rows(logits), dt, T, E, _ld(logits), _p(topk_ids), K, sc,
                                         int(bool(renorm)), scale, _rows(dlogits), _ld(dlogits), _p(dev_status),
                                         _s(stream)))
+
+
+def _slots(cu_seqlens, slot_order, rep_expert):
+    """(cu_seqlens, n_slots, slot_order, rep_expert, n_rep) of a call over slots."""
+    for t in (cu_seqlens, slot_order, rep_expert):
+        if t is not None:
+            _dtype(t, torch.int32)
+    n = max(0, cu_seqlens.numel() - 1)
+    if slot_order is not None:
+        _shape("slot_order", slot_order, n)
+    return _p(cu_seqlens), n, _p(slot_order), _p(rep_expert), 0 if rep_expert is None else rep_expert.numel()
+
+
+def _bf16(*ts):
+    for t in ts:
+        if t is not None:
+            _dtype(t, torch.bfloat16)
+
+
+def ep_expert_gemm(x, w, cu_seqlens, y, transpose_w=False, slot_order=None, rep_expert=None, dev_status=None,
+                   stream=None):
+    """y[r] = x[r] W^T over the rows of each slot, W = w[e] of the slot's expert
+    (w [E, N, K]), or with transpose_w y[r] = x[r] W (w [E, K, N])."""
+    _bf16(x, w, y)
+    rows, K = x.shape
+    E, N = w.shape[0], w.shape[2 if transpose_w else 1]
+    _shape("w", w, *((E, K, N) if transpose_w else (E, N, K)))
+    _shape("y", y, rows, N)
+    with _device_of(x, w, y, cu_seqlens, slot_order, rep_expert, dev_status):
+        cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
+        _check("ep_expert_gemm", lib().ep_expert_gemm(_p(x), rows, K, _p(w), E, N, int(bool(transpose_w)), cu, n,
+                                                      order, rep, n_rep, _p(y), _p(dev_status), _s(stream)))
+
+
+def ep_expert_up(x, w, cu_seqlens, h, gu=None, slot_order=None, rep_expert=None, dev_status=None, stream=None):
+    """h[r] = silu(g) * u with (g, u) = x[r] W^T over the rows of each slot;
+    w [E, 2I, H], gate rows first; gu [rows, 2I] keeps (g, u) for the backward."""
+    _bf16(x, w, h, gu)
+    rows, H = x.shape
+    E, I = w.shape[0], h.shape[1]
+    _shape("w", w, E, 2 * I, H)
+    _shape("h", h, rows, I)
+    if gu is not None:
+        _shape("gu", gu, rows, 2 * I)
+    with _device_of(x, w, h, gu, cu_seqlens, slot_order, rep_expert, dev_status):
+        cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
+        _check("ep_expert_up", lib().ep_expert_up(_p(x), rows, H, _p(w), E, I, cu, n, order, rep, n_rep, _p(h),
+                                                  _p(gu), _p(dev_status), _s(stream)))
+
+
+def ep_expert_up_backward(dy, w2, gu, cu_seqlens, dgu, h=None, slot_order=None, rep_expert=None, dev_status=None,
+                          stream=None):
+    """dgu [rows, 2I] from dy [rows, H] through w2 [E, H, I] and the activation
+    of the kept gu; h gets the activation again (for w2's gradient)."""
+    _bf16(dy, w2, gu, dgu, h)
+    rows, H = dy.shape
+    E, _, I = w2.shape
+    _shape("w2", w2, E, H, I)
+    _shape("gu", gu, rows, 2 * I)
+    _shape("dgu", dgu, rows, 2 * I)
+    if h is not None:
+        _shape("h", h, rows, I)
+    with _device_of(dy, w2, gu, dgu, h, cu_seqlens, slot_order, rep_expert, dev_status):
+        cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
+        _check("ep_expert_up_backward",
+               lib().ep_expert_up_backward(_p(dy), rows, H, _p(w2), E, I, _p(gu), cu, n, order, rep, n_rep, _p(dgu),
+                                           _p(h), _p(dev_status), _s(stream)))
+
+
+def _grad_rows(what, g, M, N):
+    """Pointer and row stride of per-expert gradients [n, M, N]; rows contiguous, any stride between them."""
+    if g.dim() != 3 or tuple(g.shape[1:]) != (M, N) or not g[:1].is_contiguous():
+        raise ValueError(f"{what}: expected [n, {M}, {N}] with contiguous rows")
+    if not g.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return ctypes.c_void_p(g.data_ptr()), g.stride(0) if g.shape[0] > 1 else max(g.stride(0), M * N)
+
+
+def ep_expert_wgrad(a, b, cu_seqlens, g_home, g_rep=None, accumulate=False, slot_order=None, rep_expert=None,
+                    dev_status=None, stream=None):
+    """a_s^T b_s of every slot s, into g_home[e] (home copies) and g_rep[m]
+    (replica m); g_home [E, M, N] fp32 and g_rep [cap, M, N] fp32 or bf16 may be
+    parts of longer rows (a stride between experts).  rep_expert is not read: a
+    replica's gradient has its own row."""
+    _bf16(a, b)
+    _dtype(g_home, torch.float32)
+    rows, M = a.shape
+    N = b.shape[1]
+    _shape("b", b, rows, N)
+    home, ld_home = _grad_rows("g_home", g_home, M, N)
+    rep, ld_rep, n_rep, dt = None, 0, 0, EP_DTYPE_F32
+    if g_rep is not None:
+        _dtype(g_rep, torch.float32, torch.bfloat16)
+        rep, ld_rep = _grad_rows("g_rep", g_rep, M, N)
+        n_rep = g_rep.shape[0]
+        dt = EP_DTYPE_F32 if g_rep.dtype == torch.float32 else EP_DTYPE_BF16
+    with _device_of(a, b, cu_seqlens, g_home, g_rep, slot_order, dev_status):
+        cu, n, order, _, _ = _slots(cu_seqlens, slot_order, None)
+        _check("ep_expert_wgrad",
+               lib().ep_expert_wgrad(_p(a), _p(b), rows, M, N, cu, n, order, home, g_home.shape[0], ld_home, rep, dt,
+                                     n_rep, ld_rep, int(bool(accumulate)), _p(dev_status), _s(stream)))
 
 
 def ep_selftest_lookback_timeout(topk_ids, E, loads, max_vio, ws, dev_status, stream=None):

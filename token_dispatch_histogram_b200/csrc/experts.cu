@@ -1,0 +1,628 @@
+// The experts' products between dispatch and combine, and their gradients, over
+// the slots of the dispatch buffer (home experts and replicas, each a run of
+// consecutive rows): for every slot s with weights W of its expert
+//   ep_expert_gemm         y_s = x_s W^T, or x_s W
+//   ep_expert_up           h_s = silu(x_s Wg^T) * (x_s Wu^T)
+//   ep_expert_up_backward  the gradient of that, from dy_s W2
+//   ep_expert_wgrad        g_s = a_s^T b_s, fp32
+//
+// One persistent kernel per form, one CTA per SM, two CTAs (a cluster) on one
+// tile of 256 x 256: each holds half of both operands and half of the result's
+// rows.  Alone, a CTA with a 128 x 256 tile would read 12 KB of operands per
+// product of 128 cycles and write as much for the next, more than the 128 bytes
+// per cycle its shared memory takes; a pair shares the second operand and needs
+// 8 KB each.  A pair walks output tiles in a fixed order; the slots' row counts
+// are on the device, so every CTA first scans them into shared memory (tiles
+// before each slot) and finds a tile's slot there by bisection: no launch depends
+// on a count the host would have to read.  In each CTA warp 0 brings operand
+// tiles of 64 along the contraction into a ring in shared memory (TMA, 128-byte
+// swizzle); the leader's warp 1 issues the tensor-core products into one of two
+// accumulators in tensor memory; warps 4-11 take the other accumulator through
+// the epilogue to global memory meanwhile.
+//
+// A tile's rows are its slot's rows from a multiple of 256 on; rows behind the
+// slot's end belong to the next slot and only make accumulator rows that are
+// not stored.  In the weight gradient the rows are the contraction: there the
+// lines behind the slot's end are zeroed in shared memory (in both operands, so
+// that an infinity or NaN of the next slot takes no part) by warp 3.
+//
+// The accumulator's additions cut off rather than round: over n rows of one sign
+// the sum comes out about n * 4.5e-9 too small (measured: 1.0e-5 at 4096 rows,
+// 7.4e-5 at 16,384).  bf16 results do not see that; the weight gradient is fp32
+// and may run over a hundred thousand rows, so it takes the accumulator out
+// every 512 rows (4e-7) and adds these partial sums in registers.
+#include <cuda.h>
+
+#include "umma.cuh"
+
+namespace ep {
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool encode_tiles(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box) {
+  static const EncodeTiled encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return (EncodeTiled)fn;
+  }();
+  if (!encode) return false;
+  const cuuint32_t unit[3] = {1, 1, 1};
+  cuuint64_t d[3], s[2];
+  cuuint32_t b[3];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i) s[i - 1] = strides[i - 1];
+  }
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, s, b, unit,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int TM = 256, TN = 256, TK = 64;  // of a pair of CTAs; each has TM / 2 rows of A, TN / 2 of B
+constexpr int EXP_THREADS = 384;
+constexpr int EXP_STAGES = 6;
+constexpr uint32_t A_BYTES = TM / 2 * TK * 2, B_BYTES = TN / 2 * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int PART = 8;  // WGRAD: blocks of TK rows that the accumulator sums by itself
+constexpr int MAX_SLOTS = 2 * EP_MAX_EXPERTS + EP_MAX_RANKS - 1;  // E homes and E + R - 1 replicas
+constexpr int BAND = 8;  // tiles of a slot are walked in bands of 8 row blocks, so that the CTAs at work at a
+                         // time share both operands in L2
+
+// What a product is made of: how B is held, and what happens to a finished tile.
+enum Form { Y_NT, Y_NN, UP, UP_BACKWARD, WGRAD };
+
+struct ExpertArgs {
+  int64_t rows;
+  int N, K;          // columns of the result (UP: of h), contraction (WGRAD: N columns, M = K rows of the result)
+  int n_slots, n_w, n_rep;
+  const int32_t *cu, *slots, *rep;
+  uint16_t *y, *y2;  // Y: y; UP: h, gu or NULL; UP_BACKWARD: dgu, h or NULL
+  const uint16_t* gu;
+  float* g_home;
+  void* g_rep;
+  int64_t ld_home, ld_rep;  // elements between experts
+  bool rep_bf16, accumulate;
+  int32_t* dev_status;
+};
+
+// Rows [begin, begin + len) of slot s and where its weights (or its gradient) are: w < n_w the expert of the
+// weights; for WGRAD the slot id itself.  len < 0: no such slot, nothing to do.
+struct Slot {
+  int64_t begin;
+  int len, w;
+};
+
+template <Form F>
+__device__ __forceinline__ Slot load_slot(const ExpertArgs& a, int s, int32_t* bits) {
+  const int id = a.slots ? __ldg(a.slots + s) : s;
+  Slot r{0, -1, id};
+  if (id < 0) return r;
+  if (id >= a.n_w + a.n_rep || (id >= a.n_w && F != WGRAD && !a.rep)) {
+    *bits |= EP_DEV_BAD_EXPERT_ID;
+    return r;
+  }
+  if (F != WGRAD && id >= a.n_w) {
+    r.w = __ldg(a.rep + (id - a.n_w));
+    if (r.w < 0 || r.w >= a.n_w) {
+      *bits |= EP_DEV_BAD_EXPERT_ID;
+      return r;
+    }
+  }
+  const int b = __ldg(a.cu + s), e = __ldg(a.cu + s + 1);
+  if (b < 0 || e < b || e > a.rows) {
+    *bits |= EP_DEV_BAD_ROW;
+    return r;
+  }
+  r.begin = b;
+  r.len = e - b;
+  return r;
+}
+
+struct Tile {
+  Slot slot;
+  int m, n;  // first row (within the slot; WGRAD: of the result) and column
+  int steps; // blocks of TK along the contraction
+};
+
+struct ExpertShared {
+  uint64_t full[EXP_STAGES];   // the leader's: both CTAs' operands of a stage are there
+  uint64_t empty[EXP_STAGES];  // the products have read a stage
+  uint64_t tail[EXP_STAGES];   // WGRAD: this CTA's operands of a slot's last stage are there, to be cut
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];       // the leader's: both CTAs have taken an accumulator out
+  uint32_t tmem;
+  int abort;
+  int32_t warp_sums[32];
+  int32_t before[MAX_SLOTS + 1];  // tiles before each slot
+};
+
+// A bounded wait of a whole warp that gives up as soon as another role of the CTA has.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ExpertShared* sh, int32_t* dev_status) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!(ok = mbar_try_wait(bar, parity))) {
+      if (*(volatile int*)&sh->abort) break;
+      if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+        *(volatile int*)&sh->abort = 1;
+        flag(dev_status, EP_DEV_COPY_TIMEOUT);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+template <Form F>
+__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const ExpertShared* sh, int t, int* hint) {
+  int lo = *hint, hi = a.n_slots - 1;  // the last slot with before[s] <= t; tiles come in ascending order
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sh->before[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  *hint = lo;
+  int32_t ignore = 0;
+  Tile r;
+  r.slot = load_slot<F>(a, lo, &ignore);
+  constexpr int tn = F == UP ? TN / 2 : TN;
+  const int nb = (a.N + tn - 1) / tn;
+  const int mb = ((F == WGRAD ? a.K : r.slot.len) + TM - 1) / TM;
+  const int i = t - sh->before[lo];
+  const int band = i / (BAND * nb), in_band = i - band * BAND * nb;
+  const int height = min(BAND, mb - band * BAND);
+  r.n = in_band / height * tn;
+  r.m = (band * BAND + in_band % height) * TM;
+  r.steps = ((F == WGRAD ? r.slot.len : a.K) + TK - 1) / TK;
+  return r;
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
+                    f32x2_to_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void unpack8(uint4 p, float* v) {
+  const uint32_t u[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_bits_to_f32(u[i] & 0xffffu);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+// 1 / (1 + e^-g); e^-g overflows to infinity for g below -88, where the result is 0
+__device__ __forceinline__ float sigmoid_fast(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+// One chunk of 8 columns of a finished row, from fp32.
+template <Form F>
+__device__ __forceinline__ void store8(const ExpertArgs& a, int64_t row, int n, const float* v, const float* w) {
+  if (F == Y_NT || F == Y_NN) {
+    *reinterpret_cast<uint4*>(a.y + row * a.N + n) = pack8(v);
+  } else if (F == UP) {
+    float h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = v[j] * sigmoid_fast(v[j]) * w[j];
+    *reinterpret_cast<uint4*>(a.y + row * a.N + n) = pack8(h);
+    if (a.y2) {
+      uint16_t* gu = a.y2 + row * 2 * a.N + n;
+      *reinterpret_cast<uint4*>(gu) = pack8(v);
+      *reinterpret_cast<uint4*>(gu + a.N) = pack8(w);
+    }
+  } else {
+    const uint16_t* gu = a.gu + row * 2 * a.N + n;
+    float g[8], u[8], dg[8], du[8], h[8];
+    unpack8(ld_stream_v4(gu), g);
+    unpack8(ld_stream_v4(gu + a.N), u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float sg = sigmoid_fast(g[j]), si = g[j] * sg;
+      dg[j] = v[j] * u[j] * (sg + si * (1.f - sg));
+      du[j] = v[j] * si;
+      h[j] = si * u[j];
+    }
+    uint16_t* to = a.y + row * 2 * a.N + n;
+    *reinterpret_cast<uint4*>(to) = pack8(dg);
+    *reinterpret_cast<uint4*>(to + a.N) = pack8(du);
+    if (a.y2) *reinterpret_cast<uint4*>(a.y2 + row * a.N + n) = pack8(h);
+  }
+}
+
+__device__ __forceinline__ void store_grad8(const ExpertArgs& a, int id, int64_t at, const float* s) {
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = s[j];
+  const bool home = id < a.n_w;
+  if (home || !a.rep_bf16) {
+    float4* to = reinterpret_cast<float4*>(home ? a.g_home + (int64_t)id * a.ld_home + at
+                                                : (float*)a.g_rep + (int64_t)(id - a.n_w) * a.ld_rep + at);
+    if (a.accumulate) {
+      const float4 l = to[0], h = to[1];
+      v[0] += l.x, v[1] += l.y, v[2] += l.z, v[3] += l.w;
+      v[4] += h.x, v[5] += h.y, v[6] += h.z, v[7] += h.w;
+    }
+    to[0] = make_float4(v[0], v[1], v[2], v[3]);
+    to[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint4* to = reinterpret_cast<uint4*>((uint16_t*)a.g_rep + (int64_t)(id - a.n_w) * a.ld_rep + at);
+    if (a.accumulate) {
+      float o[8];
+      unpack8(*to, o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += o[j];
+    }
+    *to = pack8(v);
+  }
+}
+
+template <Form F>
+__global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
+    k_experts(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+              const __grid_constant__ ExpertArgs a) {
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
+  ExpertShared* sh = reinterpret_cast<ExpertShared*>(ring + EXP_STAGES * STAGE_BYTES);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)pair_rank(), first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  constexpr int tn = F == UP ? TN / 2 : TN;
+
+  if (tid == 0) {
+    for (int i = 0; i < EXP_STAGES; ++i) {
+      mbar_init(&sh->full[i], 2);
+      mbar_init(&sh->empty[i], 1);
+      mbar_init(&sh->tail[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->acc_full[i], 1);
+      mbar_init(&sh->acc_empty[i], 2 * 8);
+    }
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc(&sh->tmem, 2 * TN);
+  int32_t bits = 0;
+  {
+    const int nb = (a.N + tn - 1) / tn;
+    for (int s = tid; s < a.n_slots; s += EXP_THREADS) {
+      const Slot slot = load_slot<F>(a, s, &bits);
+      const int mb = slot.len < 0 ? 0 : ((F == WGRAD ? a.K : slot.len) + TM - 1) / TM;
+      sh->before[s] = F == WGRAD && a.accumulate && slot.len == 0 ? 0 : mb * nb;
+    }
+  }
+  if (bits && blockIdx.x == 0) flag(a.dev_status, bits);
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  const int total = block_scan_array(sh->before, a.n_slots, sh->warp_sums);
+  const uint32_t tmem = sh->tmem;
+  pair_sync();  // the other CTA's barriers are set up
+
+  if (warp == 0) {
+    // ---- this CTA's operand tiles into the ring
+    int stage = 0, hint = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < total; t += step) {
+      const Tile tile = find_tile<F>(a, sh, t, &hint);
+      // rows behind the slot's end need not be read where a whole half is
+      const bool rows = F == WGRAD || tile.m + rank * (TM / 2) < tile.slot.len;
+      for (int k = 0; k < tile.steps; ++k) {
+        if (!(ok = wait_or_abort(&sh->empty[stage], phase ^ 1, sh, a.dev_status))) break;
+        if (lane == 0) {
+          uint8_t* sa = ring + stage * STAGE_BYTES;
+          uint8_t* sb = sa + A_BYTES;
+          const int kk = k * TK;
+          const bool tail = F == WGRAD && kk + TK > tile.slot.len;
+          const uint32_t bar = tail ? smem_addr(&sh->tail[stage]) : leader_addr(&sh->full[stage]);
+          pair_arrive_expect_tx(bar, rows ? STAGE_BYTES : B_BYTES);
+          if (F == WGRAD) {
+            const int row = (int)tile.slot.begin + kk;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              tma_tile_2d(sa + i * 8192, &map_a, bar, tile.m + rank * (TM / 2) + i * 64, row);
+              tma_tile_2d(sb + i * 8192, &map_b, bar, tile.n + rank * (TN / 2) + i * 64, row);
+            }
+          } else {
+            if (rows) tma_tile_2d(sa, &map_a, bar, kk, (int)tile.slot.begin + tile.m + rank * (TM / 2));
+            if (F == UP) {  // the leader holds the gate's rows, the other CTA the up projection's
+              tma_tile_3d(sb, &map_b, bar, kk, rank * a.N + tile.n, tile.slot.w);
+            } else if (F == Y_NT) {
+              tma_tile_3d(sb, &map_b, bar, kk, tile.n + rank * (TN / 2), tile.slot.w);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                tma_tile_3d(sb + i * 8192, &map_b, bar, tile.n + rank * (TN / 2) + i * 64, kk, tile.slot.w);
+            }
+          }
+        }
+        __syncwarp();
+        if (++stage == EXP_STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---- tensor-core products (the whole warp walks, lane 0 issues)
+    constexpr bool a_m = F == WGRAD, b_n = F == WGRAD || F == Y_NN || F == UP_BACKWARD;
+    constexpr uint32_t idesc = umma_idesc(TM, TN, a_m, b_n);
+    int stage = 0, hint = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < total; t += step) {
+      const Tile tile = find_tile<F>(a, sh, t, &hint);
+      for (int k = 0; k < tile.steps; ++k) {
+        const int part = F == WGRAD ? k % PART : k;
+        if (part == 0) {
+          if (!(ok = wait_or_abort(&sh->acc_empty[acc], acc_phase ^ 1, sh, a.dev_status))) break;
+        }
+        if (!(ok = wait_or_abort(&sh->full[stage], phase, sh, a.dev_status))) break;
+        umma_fence_after();
+        if (lane == 0) {
+          const uint32_t sa = smem_addr(ring + stage * STAGE_BYTES), sb = sa + A_BYTES;
+          const uint64_t da = a_m ? umma_smem_desc(sa, 8192, 1024) : umma_smem_desc(sa, 16, 1024);
+          const uint64_t db = b_n ? umma_smem_desc(sb, 8192, 1024) : umma_smem_desc(sb, 16, 1024);
+#pragma unroll
+          for (int i = 0; i < TK / 16; ++i)  // 16 elements on: 32 bytes along K, two groups of 8 lines otherwise
+            umma_bf16(tmem + acc * TN, da + (a_m ? i * 128 : i * 2), db + (b_n ? i * 128 : i * 2), idesc,
+                      part > 0 || i > 0);
+          umma_commit(&sh->empty[stage]);
+        }
+        __syncwarp();
+        if (++stage == EXP_STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (k + 1 == tile.steps || (F == WGRAD && part + 1 == PART)) {
+          if (lane == 0) umma_commit(&sh->acc_full[acc]);
+          __syncwarp();
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1;
+          }
+        }
+      }
+    }
+  } else if (F == WGRAD && warp == 3) {
+    // ---- zero the lines behind a slot's end in its last block of rows
+    int hint = 0, block = 0;  // blocks of rows so far: block % stages is the stage
+    uint32_t phases = 0;
+    for (int t = first; t < total; t += step) {
+      const Tile tile = find_tile<F>(a, sh, t, &hint);
+      block += tile.steps;
+      const int valid = tile.slot.len % TK;
+      if (valid == 0) continue;
+      const int stage = (block - 1) % EXP_STAGES;
+      if (!wait_or_abort(&sh->tail[stage], phases >> stage & 1, sh, a.dev_status)) break;
+      phases ^= 1u << stage;
+      uint8_t* s = ring + stage * STAGE_BYTES;
+      for (int i = lane; i < (TK - valid) * 8; i += 32) {
+#pragma unroll
+        for (int c = 0; c < (int)STAGE_BYTES / 8192; ++c)
+          *reinterpret_cast<uint4*>(s + c * 8192 + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) pair_arrive_release(leader_addr(&sh->full[stage]));
+    }
+  } else if (warp >= 4) {
+    // ---- finished tiles to global memory: thread = row of this CTA's half, half of its columns
+    const int row = (warp & 3) * 32 + lane;
+    const int col = warp >= 8 ? tn / 2 : 0;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 * (warp % 4), in the address's high half
+    int hint = 0, acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < total; t += step) {
+      const Tile tile = find_tile<F>(a, sh, t, &hint);
+      const int m = tile.m + rank * (TM / 2) + row;
+      const bool live = m < (F == WGRAD ? a.K : tile.slot.len);
+      if (F == WGRAD) {
+        float sum[TN / 2];
+#pragma unroll
+        for (int i = 0; i < TN / 2; ++i) sum[i] = 0.f;
+        for (int k = 0; k < tile.steps; k += PART) {
+          if (!(ok = wait_or_abort(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
+          umma_fence_after();
+#pragma unroll
+          for (int c = 0; c < TN / 2; c += 32) {
+            uint32_t r[32];
+            tmem_load32(tmem + lanes + acc * TN + col + c, r);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(r[i]);
+          }
+          umma_fence_before();
+          __syncwarp();
+          if (lane == 0) pair_arrive(leader_addr(&sh->acc_empty[acc]));
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < TN / 2; i += 8)
+            if (tile.n + col + i < a.N) store_grad8(a, tile.slot.w, (int64_t)m * a.N + tile.n + col + i, sum + i);
+        }
+        __syncwarp();
+      } else {
+        if (!(ok = wait_or_abort(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
+        umma_fence_after();
+        const uint32_t src = tmem + lanes + acc * TN + col;
+        for (int c = 0; c < tn / 2; c += 32) {
+          uint32_t r[32], u[32];
+          tmem_load32(src + c, r);
+          if (F == UP) tmem_load32(src + TN / 2 + c, u);
+          tmem_wait_load();
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              const int n = tile.n + col + c + i;
+              float v[8], w[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                v[j] = __uint_as_float(r[i + j]);
+                w[j] = F == UP ? __uint_as_float(u[i + j]) : 0.f;
+              }
+              if (n < a.N) store8<F>(a, tile.slot.begin + m, n, v, w);
+            }
+          }
+          __syncwarp();
+        }
+        umma_fence_before();
+        __syncwarp();
+        if (lane == 0) pair_arrive(leader_addr(&sh->acc_empty[acc]));
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  if (sh->abort && tid == 0) {
+    // a wait ran out: give copies and products in flight time to land before the memory is given back
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < WAIT_LIMIT_NS / 10) {
+    }
+  }
+  __syncthreads();
+  pair_sync();  // nothing of the other CTA's reaches for this one's shared or tensor memory any more
+  if (warp == 2) tmem_free(tmem, 2 * TN);
+}
+
+constexpr size_t EXP_SMEM = 1024 + EXP_STAGES * STAGE_BYTES + sizeof(ExpertShared);
+
+template <Form F>
+static int launch_experts(const CUtensorMap& ma, const CUtensorMap& mb, const ExpertArgs& a, cudaStream_t stream) {
+  if (!raise_smem_limit((const void*)k_experts<F>, EXP_SMEM)) return EP_ERR_CUDA;
+  k_experts<F><<<num_sms() / 2 * 2, EXP_THREADS, EXP_SMEM, stream>>>(ma, mb, a);
+  count_launch();
+  return launch_status();
+}
+
+// x as tiles of 64 columns and W, rows x cols per expert, along K or along N.
+static bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int cols, int box_rows) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)cols * 2};
+  const uint32_t box[2] = {64, (uint32_t)box_rows};
+  return encode_tiles(m, p, 2, dims, strides, box);
+}
+
+static bool map_weights(CUtensorMap* m, const void* p, int n, int rows, int cols, int box_rows) {
+  const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)n};
+  const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)rows * cols * 2};
+  const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+  return encode_tiles(m, p, 3, dims, strides, box);
+}
+
+static bool valid_slots(int64_t rows, int n_w, const int32_t* cu, int n_slots, int n_rep) {
+  return rows >= 0 && rows < ((int64_t)1 << 31) - 1024 && n_w >= 1 && n_w <= EP_MAX_EXPERTS && n_slots >= 0 &&
+         n_slots <= MAX_SLOTS && n_rep >= 0 && n_rep <= MAX_SLOTS && (n_slots == 0 || cu);
+}
+
+// Widths are multiples of 8 (16-byte rows) and small enough that a coordinate, or 2 * width, fits 31 bits with room.
+static bool valid_width(int64_t n) { return n >= 8 && n % 8 == 0 && n <= (1 << 28); }
+
+// Tiles of a call fit 31 bits, and an expert's weights the strides of a tensor map.
+static bool valid_extent(int64_t row_blocks, int64_t m, int64_t n) {
+  return row_blocks * ((n + TN / 2 - 1) / (TN / 2)) < ((int64_t)1 << 30) && m * n < ((int64_t)1 << 38);
+}
+
+static bool null_or_misaligned(const void* p) { return !p || !aligned16(p); }
+
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_expert_gemm(const uint16_t* x, int64_t rows, int64_t K, const uint16_t* w, int n_w, int64_t N,
+                              int transpose_w, const int32_t* cu_seqlens, int n_slots, const int32_t* slot_order,
+                              const int32_t* rep_expert, int n_rep, uint16_t* y, int32_t* dev_status,
+                              cudaStream_t stream) {
+  if (!valid_slots(rows, n_w, cu_seqlens, n_slots, n_rep) || !valid_width(K) || !valid_width(N)) return EP_ERR_ARG;
+  if (!valid_extent(rows / TM + n_slots, K, N)) return EP_ERR_ARG;
+  if (rows == 0 || n_slots == 0) return EP_OK;
+  if (null_or_misaligned(x) || null_or_misaligned(w) || null_or_misaligned(y)) return EP_ERR_ARG;
+  ExpertArgs a = {};
+  a.rows = rows, a.N = (int)N, a.K = (int)K, a.n_slots = n_slots, a.n_w = n_w, a.n_rep = rep_expert ? n_rep : 0;
+  a.cu = cu_seqlens, a.slots = slot_order, a.rep = rep_expert, a.y = y, a.dev_status = dev_status;
+  CUtensorMap ma, mb;
+  if (!map_rows(&ma, x, rows, (int)K, TM / 2)) return EP_ERR_CUDA;
+  if (transpose_w) {
+    if (!map_weights(&mb, w, n_w, (int)K, (int)N, TK)) return EP_ERR_CUDA;
+    return launch_experts<Y_NN>(ma, mb, a, stream);
+  }
+  if (!map_weights(&mb, w, n_w, (int)N, (int)K, TN / 2)) return EP_ERR_CUDA;
+  return launch_experts<Y_NT>(ma, mb, a, stream);
+}
+
+extern "C" int ep_expert_up(const uint16_t* x, int64_t rows, int64_t H, const uint16_t* w, int n_w, int64_t I,
+                            const int32_t* cu_seqlens, int n_slots, const int32_t* slot_order,
+                            const int32_t* rep_expert, int n_rep, uint16_t* h, uint16_t* gu, int32_t* dev_status,
+                            cudaStream_t stream) {
+  if (!valid_slots(rows, n_w, cu_seqlens, n_slots, n_rep) || !valid_width(H) || !valid_width(I)) return EP_ERR_ARG;
+  if (!valid_extent(rows / TM + n_slots, H, I)) return EP_ERR_ARG;
+  if (rows == 0 || n_slots == 0) return EP_OK;
+  if (null_or_misaligned(x) || null_or_misaligned(w) || null_or_misaligned(h) || !aligned16(gu)) return EP_ERR_ARG;
+  ExpertArgs a = {};
+  a.rows = rows, a.N = (int)I, a.K = (int)H, a.n_slots = n_slots, a.n_w = n_w, a.n_rep = rep_expert ? n_rep : 0;
+  a.cu = cu_seqlens, a.slots = slot_order, a.rep = rep_expert, a.y = h, a.y2 = gu, a.dev_status = dev_status;
+  CUtensorMap ma, mb;
+  if (!map_rows(&ma, x, rows, (int)H, TM / 2) || !map_weights(&mb, w, n_w, (int)(2 * I), (int)H, TN / 2))
+    return EP_ERR_CUDA;
+  return launch_experts<UP>(ma, mb, a, stream);
+}
+
+extern "C" int ep_expert_up_backward(const uint16_t* dy, int64_t rows, int64_t H, const uint16_t* w2, int n_w,
+                                     int64_t I, const uint16_t* gu, const int32_t* cu_seqlens, int n_slots,
+                                     const int32_t* slot_order, const int32_t* rep_expert, int n_rep, uint16_t* dgu,
+                                     uint16_t* h, int32_t* dev_status, cudaStream_t stream) {
+  if (!valid_slots(rows, n_w, cu_seqlens, n_slots, n_rep) || !valid_width(H) || !valid_width(I)) return EP_ERR_ARG;
+  if (!valid_extent(rows / TM + n_slots, H, I)) return EP_ERR_ARG;
+  if (rows == 0 || n_slots == 0) return EP_OK;
+  if (null_or_misaligned(dy) || null_or_misaligned(w2) || null_or_misaligned(gu) || null_or_misaligned(dgu) ||
+      !aligned16(h))
+    return EP_ERR_ARG;
+  ExpertArgs a = {};
+  a.rows = rows, a.N = (int)I, a.K = (int)H, a.n_slots = n_slots, a.n_w = n_w, a.n_rep = rep_expert ? n_rep : 0;
+  a.cu = cu_seqlens, a.slots = slot_order, a.rep = rep_expert, a.y = dgu, a.y2 = h, a.gu = gu;
+  a.dev_status = dev_status;
+  CUtensorMap ma, mb;
+  if (!map_rows(&ma, dy, rows, (int)H, TM / 2) || !map_weights(&mb, w2, n_w, (int)H, (int)I, TK)) return EP_ERR_CUDA;
+  return launch_experts<UP_BACKWARD>(ma, mb, a, stream);
+}
+
+extern "C" int ep_expert_wgrad(const uint16_t* a_rows, const uint16_t* b_rows, int64_t rows, int64_t M, int64_t N,
+                               const int32_t* cu_seqlens, int n_slots, const int32_t* slot_order, float* g_home,
+                               int n_home, int64_t ld_home, void* g_rep, int rep_dtype, int n_rep, int64_t ld_rep,
+                               int accumulate, int32_t* dev_status, cudaStream_t stream) {
+  if (!valid_slots(rows, n_home, cu_seqlens, n_slots, n_rep) || !valid_width(M) || !valid_width(N)) return EP_ERR_ARG;
+  if (rep_dtype != EP_DTYPE_F32 && rep_dtype != EP_DTYPE_BF16) return EP_ERR_ARG;
+  if (!valid_extent((M + TM - 1) / TM * n_slots, M, N) || ld_home < M * N || ld_home % 4) return EP_ERR_ARG;
+  if (g_rep && (!aligned16(g_rep) || ld_rep < M * N || ld_rep % (rep_dtype == EP_DTYPE_F32 ? 4 : 8))) return EP_ERR_ARG;
+  if (n_slots == 0) return EP_OK;
+  if (null_or_misaligned(g_home) || (rows > 0 && (null_or_misaligned(a_rows) || null_or_misaligned(b_rows))))
+    return EP_ERR_ARG;
+  ExpertArgs a = {};
+  a.rows = rows, a.N = (int)N, a.K = (int)M, a.n_slots = n_slots, a.n_w = n_home, a.n_rep = g_rep ? n_rep : 0;
+  a.cu = cu_seqlens, a.slots = slot_order, a.g_home = g_home, a.g_rep = g_rep, a.ld_home = ld_home, a.ld_rep = ld_rep;
+  a.rep_bf16 = rep_dtype == EP_DTYPE_BF16, a.accumulate = accumulate != 0, a.dev_status = dev_status;
+  CUtensorMap ma, mb;
+  // without rows nothing is read, but a map needs an address
+  if (!map_rows(&ma, rows ? (const void*)a_rows : g_home, rows ? rows : 1, (int)M, TK) ||
+      !map_rows(&mb, rows ? (const void*)b_rows : g_home, rows ? rows : 1, (int)N, TK))
+    return EP_ERR_CUDA;
+  return launch_experts<WGRAD>(ma, mb, a, stream);
+}
