@@ -13,12 +13,12 @@
 // per cycle its shared memory takes; a pair shares the second operand and needs
 // 8 KB each.  A pair walks output tiles in a fixed order; the slots' row counts
 // are on the device, so every CTA first scans them into shared memory (tiles
-// before each slot) and finds a tile's slot there by bisection: no launch depends
-// on a count the host would have to read.  In each CTA warp 0 brings operand
-// tiles of 64 along the contraction into a ring in shared memory (TMA, 128-byte
-// swizzle); the leader's warp 1 issues the tensor-core products into one of two
-// accumulators in tensor memory; warps 4-11 take the other accumulator through
-// the epilogue to global memory meanwhile.
+// before each slot) and finds a tile's slot there by bisection (warp 2, some tiles
+// ahead): no launch depends on a count the host would have to read.  In each CTA
+// warp 0 brings operand tiles of 64 along the contraction into a ring in shared
+// memory (TMA, 128-byte swizzle); the leader's warp 1 issues the tensor-core
+// products into one of two accumulators in tensor memory; warps 4-11 take the
+// other accumulator through the epilogue to global memory meanwhile.
 //
 // A tile's rows are its slot's rows from a multiple of 256 on; rows behind the
 // slot's end belong to the next slot and only make accumulator rows that are
@@ -69,6 +69,7 @@ constexpr int TM = 256, TN = 256, TK = 64;  // of a pair of CTAs; each has TM / 
 constexpr int EXP_THREADS = 384;
 constexpr int EXP_STAGES = 6;
 constexpr uint32_t A_BYTES = TM / 2 * TK * 2, B_BYTES = TN / 2 * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int TILES_AHEAD = 4;
 constexpr int PART = 8;  // WGRAD: blocks of TK rows that the accumulator sums by itself
 constexpr int MAX_SLOTS = 2 * EP_MAX_EXPERTS + EP_MAX_RANKS - 1;  // E homes and E + R - 1 replicas
 constexpr int BAND = 8;  // tiles of a slot are walked in bands of 8 row blocks, so that the CTAs at work at a
@@ -126,8 +127,8 @@ __device__ __forceinline__ Slot load_slot(const ExpertArgs& a, int s, int32_t* b
 
 struct Tile {
   Slot slot;
-  int m, n;  // first row (within the slot; WGRAD: of the result) and column
-  int steps; // blocks of TK along the contraction
+  int m, n;   // first row (within the slot; WGRAD: of the result) and column
+  int steps;  // blocks of TK along the contraction; -1: no tile any more
 };
 
 struct ExpertShared {
@@ -137,6 +138,8 @@ struct ExpertShared {
   uint64_t tail[EXP_STAGES];   // WGRAD: this CTA's operands of a slot's last stage are there, to be cut
   uint64_t acc_full[2];
   uint64_t acc_empty[2];       // the leader's: both CTAs have taken an accumulator out
+  uint64_t tile_full[TILES_AHEAD], tile_empty[TILES_AHEAD];
+  Tile tiles[TILES_AHEAD];     // found ahead by warp 2
   uint32_t tmem;
   int abort;
   int32_t warp_sums[32];
@@ -185,6 +188,28 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const ExpertShare
   r.steps = ((F == WGRAD ? r.slot.len : a.K) + TK - 1) / TK;
   return r;
 }
+
+// A role's walk over the tiles that warp 2 finds.  next() is false at the end, or
+// when a wait ran out.
+struct Walk {
+  ExpertShared* sh;
+  int32_t* dev_status;
+  int at;
+  uint32_t phase;
+  Tile tile;
+  __device__ __forceinline__ Walk(ExpertShared* s, int32_t* st) : sh(s), dev_status(st), at(0), phase(0) {}
+  __device__ __forceinline__ bool next() {
+    if (!wait_or_abort(&sh->tile_full[at], phase, sh, dev_status)) return false;
+    tile = sh->tiles[at];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->tile_empty[at]);
+    if (++at == TILES_AHEAD) {
+      at = 0;
+      phase ^= 1;
+    }
+    return tile.steps >= 0;
+  }
+};
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
@@ -316,6 +341,10 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&sh->empty[i], 1);
       mbar_init(&sh->tail[i], 1);
     }
+    for (int i = 0; i < TILES_AHEAD; ++i) {
+      mbar_init(&sh->tile_full[i], 1);
+      mbar_init(&sh->tile_empty[i], 9 + (rank == 0) + (F == WGRAD));  // warps 0 and 4-11, 1 of the leader, 3
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->acc_full[i], 1);
       mbar_init(&sh->acc_empty[i], 2 * 8);
@@ -343,11 +372,12 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
 
   if (warp == 0) {
     // ---- this CTA's operand tiles into the ring
-    int stage = 0, hint = 0;
+    int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int t = first; ok && t < total; t += step) {
-      const Tile tile = find_tile<F>(a, sh, t, &hint);
+    Walk walk(sh, a.dev_status);
+    while (ok && walk.next()) {
+      const Tile& tile = walk.tile;
       // rows behind the slot's end need not be read where a whole half is
       const bool rows = F == WGRAD || tile.m + rank * (TM / 2) < tile.slot.len;
       for (int k = 0; k < tile.steps; ++k) {
@@ -390,11 +420,12 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     // ---- tensor-core products (the whole warp walks, lane 0 issues)
     constexpr bool a_m = F == WGRAD, b_n = F == WGRAD || F == Y_NN || F == UP_BACKWARD;
     constexpr uint32_t idesc = umma_idesc(TM, TN, a_m, b_n);
-    int stage = 0, hint = 0, acc = 0;
+    int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    for (int t = first; ok && t < total; t += step) {
-      const Tile tile = find_tile<F>(a, sh, t, &hint);
+    Walk walk(sh, a.dev_status);
+    while (ok && walk.next()) {
+      const Tile& tile = walk.tile;
       for (int k = 0; k < tile.steps; ++k) {
         const int part = F == WGRAD ? k % PART : k;
         if (part == 0) {
@@ -427,16 +458,37 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
       }
     }
+  } else if (warp == 2) {
+    // ---- the tiles, a few ahead of the other warps: a search and loads that depend on each other
+    int hint = 0, at = 0;
+    uint32_t phase = 0;
+    for (int t = first;; t += step) {
+      if (!wait_or_abort(&sh->tile_empty[at], phase ^ 1, sh, a.dev_status)) break;
+      Tile tile = {};
+      tile.steps = -1;
+      if (t < total) tile = find_tile<F>(a, sh, t, &hint);
+      if (lane == 0) {
+        sh->tiles[at] = tile;
+        mbar_arrive(&sh->tile_full[at]);
+      }
+      __syncwarp();
+      if (t >= total) break;
+      if (++at == TILES_AHEAD) {
+        at = 0;
+        phase ^= 1;
+      }
+    }
   } else if (F == WGRAD && warp == 3) {
     // ---- zero the lines behind a slot's end in its last block of rows
-    int hint = 0, block = 0;  // blocks of rows so far: block % stages is the stage
+    int block = 0;  // blocks of rows so far, modulo the stages
     uint32_t phases = 0;
-    for (int t = first; t < total; t += step) {
-      const Tile tile = find_tile<F>(a, sh, t, &hint);
-      block += tile.steps;
+    Walk walk(sh, a.dev_status);
+    while (walk.next()) {
+      const Tile& tile = walk.tile;
+      block = (block + tile.steps) % EXP_STAGES;
       const int valid = tile.slot.len % TK;
       if (valid == 0) continue;
-      const int stage = (block - 1) % EXP_STAGES;
+      const int stage = (block + EXP_STAGES - 1) % EXP_STAGES;
       if (!wait_or_abort(&sh->tail[stage], phases >> stage & 1, sh, a.dev_status)) break;
       phases ^= 1u << stage;
       uint8_t* s = ring + stage * STAGE_BYTES;
@@ -455,11 +507,12 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     const int col = warp >= 8 ? tn / 2 : 0;
     const uint32_t lanes = (uint32_t)row << 16;  // the address's high half
     Turn turn(sh->turn[warp - 4], lane);
-    int hint = 0, acc = 0;
+    int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int t = first; ok && t < total; t += step) {
-      const Tile tile = find_tile<F>(a, sh, t, &hint);
+    Walk walk(sh, a.dev_status);
+    while (ok && walk.next()) {
+      const Tile& tile = walk.tile;
       const int m = tile.m + rank * (TM / 2) + row;
       const int rows = (F == WGRAD ? a.K : tile.slot.len) - m;  // of this warp's 32, those that are stored
       if (F == WGRAD) {

@@ -58,6 +58,10 @@ __device__ __forceinline__ void tma_tile_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Arrivals on a barrier of this CTA or of the leader.  Only pair_arrive_release
 // publishes this thread's writes; the others carry no data of their own (copies
 // and products complete on barriers, tensor memory is ordered by its fences),
