@@ -67,16 +67,28 @@ bool encode_tiles(CUtensorMap* map, const void* base, int rank, const uint64_t* 
 
 constexpr int TM = 256, TN = 256, TK = 64;  // of a pair of CTAs; each has TM / 2 rows of A, TN / 2 of B
 constexpr int EXP_THREADS = 384;
-constexpr int EXP_STAGES = 6;
-constexpr uint32_t A_BYTES = TM / 2 * TK * 2, B_BYTES = TN / 2 * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr uint32_t A_BYTES = TM / 2 * TK * 2, B_BYTES = TN / 2 * TK * 2;
+constexpr uint32_t RING_BYTES = 12 * A_BYTES;  // 4 stages of an A and two B tiles, or 6 of one each
+constexpr int MAX_STAGES = 6;
 constexpr int TILES_AHEAD = 4;
 constexpr int PART = 8;  // WGRAD: blocks of TK rows that the accumulator sums by itself
 constexpr int MAX_SLOTS = 2 * EP_MAX_EXPERTS + EP_MAX_RANKS - 1;  // E homes and E + R - 1 replicas
 constexpr int BAND = 8;  // tiles of a slot are walked in bands of 8 row blocks, so that the CTAs at work at a
-                         // time share both operands in L2
+                         // time share both operands in L2 (4 to 16 measured the same)
 
 // What a product is made of: how B is held, and what happens to a finished tile.
 enum Form { Y_NT, Y_NN, UP, UP_BACKWARD, WGRAD };
+
+// Accumulators of TN columns that a tile takes at most, the stages that leaves
+// in the ring, and the result's columns in one accumulator.
+template <Form F>
+struct Shape {
+  static constexpr int halves = F == WGRAD ? 1 : 2;
+  static constexpr uint32_t stage_bytes = A_BYTES + halves * B_BYTES;
+  static constexpr int stages = RING_BYTES / stage_bytes;
+  static constexpr int tn = F == UP ? TN / 2 : TN;
+  static_assert(stages <= MAX_STAGES && RING_BYTES % stage_bytes == 0, "");
+};
 
 struct ExpertArgs {
   int64_t rows;
@@ -127,15 +139,16 @@ __device__ __forceinline__ Slot load_slot(const ExpertArgs& a, int s, int32_t* b
 
 struct Tile {
   Slot slot;
-  int m, n;   // first row (within the slot; WGRAD: of the result) and column
-  int steps;  // blocks of TK along the contraction; -1: no tile any more
+  int m, n;    // first row (within the slot; WGRAD: of the result) and column
+  int halves;  // accumulators that it takes; 0: no columns left, not a tile
+  int steps;   // blocks of TK along the contraction; -1: no tile any more
 };
 
 struct ExpertShared {
   uint4 turn[8][128];          // the epilogue warps' 32 rows of 64 bytes
-  uint64_t full[EXP_STAGES];   // the leader's: both CTAs' operands of a stage are there
-  uint64_t empty[EXP_STAGES];  // the products have read a stage
-  uint64_t tail[EXP_STAGES];   // WGRAD: this CTA's operands of a slot's last stage are there, to be cut
+  uint64_t full[MAX_STAGES];   // the leader's: both CTAs' operands of a stage are there
+  uint64_t empty[MAX_STAGES];  // the products have read a stage
+  uint64_t tail[MAX_STAGES];   // WGRAD: this CTA's operands of a slot's last stage are there, to be cut
   uint64_t acc_full[2];
   uint64_t acc_empty[2];       // the leader's: both CTAs have taken an accumulator out
   uint64_t tile_full[TILES_AHEAD], tile_empty[TILES_AHEAD];
@@ -146,25 +159,47 @@ struct ExpertShared {
   int32_t before[MAX_SLOTS + 1];  // tiles before each slot
 };
 
-// A bounded wait of a whole warp that gives up as soon as another role of the CTA has.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ExpertShared* sh, int32_t* dev_status) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!(ok = mbar_try_wait(bar, parity))) {
-      if (*(volatile int*)&sh->abort) break;
-      if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
-        *(volatile int*)&sh->abort = 1;
-        flag(dev_status, EP_DEV_COPY_TIMEOUT);
-        break;
-      }
+// A thread's bounded wait, that gives up as soon as another role of the CTA has.
+__device__ __forceinline__ bool wait_thread(uint64_t* bar, uint32_t parity, ExpertShared* sh, int32_t* dev_status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*(volatile int*)&sh->abort) return false;
+    if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+      *(volatile int*)&sh->abort = 1;
+      flag(dev_status, EP_DEV_COPY_TIMEOUT);
+      return false;
     }
   }
-  return __all_sync(0xffffffffu, ok);
+  return true;
+}
+
+// The same for a whole warp, with one outcome.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, ExpertShared* sh, int32_t* dev_status) {
+  return __all_sync(0xffffffffu, wait_thread(bar, parity, sh, dev_status));
+}
+
+// The order of a pair's work: `wide` tiles of all the columns a tile can take,
+// then `narrow` tiles of one accumulator each.  Where the last round of wide
+// tiles would keep at most half of the pairs at work, it is done in halves by
+// twice as many.
+struct Order {
+  int wide, narrow;
+};
+
+template <Form F>
+__device__ __forceinline__ Order make_order(int total, int pairs) {
+  const int last = total % pairs;
+  if (Shape<F>::halves == 1 || 2 * last > pairs) return Order{total, 0};
+  return Order{total - last, 2 * last};
 }
 
 template <Form F>
-__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const ExpertShared* sh, int t, int* hint) {
+__device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const ExpertShared* sh, const Order& o, int t,
+                                          int* hint) {
+  constexpr int tn = Shape<F>::tn, halves = Shape<F>::halves;
+  const int half = t < o.wide ? -1 : (t - o.wide) & 1;
+  if (half >= 0) t = o.wide + ((t - o.wide) >> 1);
   int lo = *hint, hi = a.n_slots - 1;  // the last slot with before[s] <= t; tiles come in ascending order
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -177,20 +212,21 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const ExpertShare
   int32_t ignore = 0;
   Tile r;
   r.slot = load_slot<F>(a, lo, &ignore);
-  constexpr int tn = F == UP ? TN / 2 : TN;
-  const int nb = (a.N + tn - 1) / tn;
+  const int nb = (a.N + halves * tn - 1) / (halves * tn);
   const int mb = ((F == WGRAD ? a.K : r.slot.len) + TM - 1) / TM;
   const int i = t - sh->before[lo];
   const int band = i / (BAND * nb), in_band = i - band * BAND * nb;
   const int height = min(BAND, mb - band * BAND);
-  r.n = in_band / height * tn;
+  r.n = in_band / height * (halves * tn) + max(half, 0) * tn;
   r.m = (band * BAND + in_band % height) * TM;
+  r.halves = r.n >= a.N ? 0 : half < 0 && halves == 2 && r.n + tn < a.N ? 2 : 1;
   r.steps = ((F == WGRAD ? r.slot.len : a.K) + TK - 1) / TK;
   return r;
 }
 
 // A role's walk over the tiles that warp 2 finds.  next() is false at the end, or
-// when a wait ran out.
+// when a wait ran out.  WARP: all lanes walk; otherwise one thread does.
+template <bool WARP>
 struct Walk {
   ExpertShared* sh;
   int32_t* dev_status;
@@ -199,10 +235,15 @@ struct Walk {
   Tile tile;
   __device__ __forceinline__ Walk(ExpertShared* s, int32_t* st) : sh(s), dev_status(st), at(0), phase(0) {}
   __device__ __forceinline__ bool next() {
-    if (!wait_or_abort(&sh->tile_full[at], phase, sh, dev_status)) return false;
-    tile = sh->tiles[at];
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->tile_empty[at]);
+    if (WARP) {
+      if (!wait_warp(&sh->tile_full[at], phase, sh, dev_status)) return false;
+      tile = sh->tiles[at];
+      __syncwarp();
+    } else {
+      if (!wait_thread(&sh->tile_full[at], phase, sh, dev_status)) return false;
+      tile = sh->tiles[at];
+    }
+    if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&sh->tile_empty[at]);
     if (++at == TILES_AHEAD) {
       at = 0;
       phase ^= 1;
@@ -246,9 +287,9 @@ struct Turn {
 };
 
 // 32 columns of bf16 (each lane its row's) to rows [0, rows) at to, columns below n
-__device__ __forceinline__ void store_rows(Turn& t, const float* v, uint16_t* to, int64_t ld, int rows, int n) {
+__device__ __forceinline__ void store_rows(Turn& t, const uint4* q, uint16_t* to, int64_t ld, int rows, int n) {
 #pragma unroll
-  for (int u = 0; u < 4; ++u) t.mine(u) = pack8(v + 8 * u);
+  for (int u = 0; u < 4; ++u) t.mine(u) = q[u];
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -256,18 +297,28 @@ __device__ __forceinline__ void store_rows(Turn& t, const float* v, uint16_t* to
   __syncwarp();
 }
 
-__device__ __forceinline__ void load_rows(Turn& t, float* v, const uint16_t* from, int64_t ld, int rows, int n) {
-  uint4 p[4];
+__device__ __forceinline__ void store_rows(Turn& t, const float* v, uint16_t* to, int64_t ld, int rows, int n) {
+  uint4 q[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) q[u] = pack8(v + 8 * u);
+  store_rows(t, q, to, ld, rows, n);
+}
+
+// The other way in two steps, so that the loads can be under way early.
+__device__ __forceinline__ void fetch_rows(const Turn& t, uint4* p, const uint16_t* from, int64_t ld, int rows, int n) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     p[j] = make_uint4(0, 0, 0, 0);
     if (t.row + 8 * j < rows && t.unit * 8 < n) p[j] = ld_stream_v4(from + (t.row + 8 * j) * ld + t.unit * 8);
   }
+}
+
+__device__ __forceinline__ void turn_rows(Turn& t, const uint4* p, uint4* q) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) t.theirs(j) = p[j];
   __syncwarp();
 #pragma unroll
-  for (int u = 0; u < 4; ++u) unpack8(t.mine(u), v + 8 * u);
+  for (int u = 0; u < 4; ++u) q[u] = t.mine(u);
   __syncwarp();
 }
 
@@ -330,13 +381,14 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
               const __grid_constant__ ExpertArgs a) {
   extern __shared__ uint8_t s_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
-  ExpertShared* sh = reinterpret_cast<ExpertShared*>(ring + EXP_STAGES * STAGE_BYTES);
+  ExpertShared* sh = reinterpret_cast<ExpertShared*>(ring + RING_BYTES);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)pair_rank(), first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  constexpr int tn = F == UP ? TN / 2 : TN;
+  constexpr int tn = Shape<F>::tn, halves = Shape<F>::halves, stages = Shape<F>::stages;
+  constexpr uint32_t stage_bytes = Shape<F>::stage_bytes;
 
   if (tid == 0) {
-    for (int i = 0; i < EXP_STAGES; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&sh->full[i], 2);
       mbar_init(&sh->empty[i], 1);
       mbar_init(&sh->tail[i], 1);
@@ -355,7 +407,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
   if (warp == 2) tmem_alloc(&sh->tmem, 2 * TN);
   int32_t bits = 0;
   {
-    const int nb = (a.N + tn - 1) / tn;
+    const int nb = (a.N + halves * tn - 1) / (halves * tn);
     for (int s = tid; s < a.n_slots; s += EXP_THREADS) {
       const Slot slot = load_slot<F>(a, s, &bits);
       const int mb = slot.len < 0 ? 0 : ((F == WGRAD ? a.K : slot.len) + TM - 1) / TM;
@@ -367,94 +419,106 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   umma_fence_after();
   const int total = block_scan_array(sh->before, a.n_slots, sh->warp_sums);
+  const Order order = make_order<F>(total, step);
   const uint32_t tmem = sh->tmem;
   pair_sync();  // the other CTA's barriers are set up
 
-  if (warp == 0) {
+  if (tid == 0) {
     // ---- this CTA's operand tiles into the ring
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    Walk walk(sh, a.dev_status);
+    Walk<false> walk(sh, a.dev_status);
     while (ok && walk.next()) {
       const Tile& tile = walk.tile;
       // rows behind the slot's end need not be read where a whole half is
       const bool rows = F == WGRAD || tile.m + rank * (TM / 2) < tile.slot.len;
+      const uint32_t bytes = tile.halves * B_BYTES + (rows ? A_BYTES : 0);
       for (int k = 0; k < tile.steps; ++k) {
-        if (!(ok = wait_or_abort(&sh->empty[stage], phase ^ 1, sh, a.dev_status))) break;
-        if (lane == 0) {
-          uint8_t* sa = ring + stage * STAGE_BYTES;
-          uint8_t* sb = sa + A_BYTES;
-          const int kk = k * TK;
-          const bool tail = F == WGRAD && kk + TK > tile.slot.len;
-          const uint32_t bar = tail ? smem_addr(&sh->tail[stage]) : leader_addr(&sh->full[stage]);
-          pair_arrive_expect_tx(bar, rows ? STAGE_BYTES : B_BYTES);
-          if (F == WGRAD) {
-            const int row = (int)tile.slot.begin + kk;
+        if (!(ok = wait_thread(&sh->empty[stage], phase ^ 1, sh, a.dev_status))) break;
+        uint8_t* sa = ring + stage * stage_bytes;
+        uint8_t* sb = sa + A_BYTES;
+        const int kk = k * TK;
+        const bool tail = F == WGRAD && kk + TK > tile.slot.len;
+        const uint32_t bar = tail ? smem_addr(&sh->tail[stage]) : leader_addr(&sh->full[stage]);
+        pair_arrive_expect_tx(bar, bytes);
+        if (F == WGRAD) {
+          const int row = (int)tile.slot.begin + kk;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              tma_tile_2d(sa + i * 8192, &map_a, bar, tile.m + rank * (TM / 2) + i * 64, row);
-              tma_tile_2d(sb + i * 8192, &map_b, bar, tile.n + rank * (TN / 2) + i * 64, row);
-            }
-          } else {
-            if (rows) tma_tile_2d(sa, &map_a, bar, kk, (int)tile.slot.begin + tile.m + rank * (TM / 2));
+          for (int i = 0; i < 2; ++i) {
+            tma_tile_2d(sa + i * 8192, &map_a, bar, tile.m + rank * (TM / 2) + i * 64, row);
+            tma_tile_2d(sb + i * 8192, &map_b, bar, tile.n + rank * (TN / 2) + i * 64, row);
+          }
+        } else {
+          if (rows) tma_tile_2d(sa, &map_a, bar, kk, (int)tile.slot.begin + tile.m + rank * (TM / 2));
+#pragma unroll
+          for (int h = 0; h < halves; ++h, sb += B_BYTES) {
+            if (h >= tile.halves) break;
+            const int n = tile.n + h * tn;
             if (F == UP) {  // the leader holds the gate's rows, the other CTA the up projection's
-              tma_tile_3d(sb, &map_b, bar, kk, rank * a.N + tile.n, tile.slot.w);
+              tma_tile_3d(sb, &map_b, bar, kk, rank * a.N + n, tile.slot.w);
             } else if (F == Y_NT) {
-              tma_tile_3d(sb, &map_b, bar, kk, tile.n + rank * (TN / 2), tile.slot.w);
+              tma_tile_3d(sb, &map_b, bar, kk, n + rank * (TN / 2), tile.slot.w);
             } else {
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                tma_tile_3d(sb + i * 8192, &map_b, bar, tile.n + rank * (TN / 2) + i * 64, kk, tile.slot.w);
+              tma_tile_3d(sb, &map_b, bar, n + rank * (TN / 2), kk, tile.slot.w);
+              tma_tile_3d(sb + 8192, &map_b, bar, n + rank * (TN / 2) + 64, kk, tile.slot.w);
             }
           }
         }
-        __syncwarp();
-        if (++stage == EXP_STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-  } else if (warp == 1 && rank == 0) {
-    // ---- tensor-core products (the whole warp walks, lane 0 issues)
+  } else if (tid == 32 && rank == 0) {
+    // ---- tensor-core products, issued by one thread: what stands between two issues is time the cores idle
     constexpr bool a_m = F == WGRAD, b_n = F == WGRAD || F == Y_NN || F == UP_BACKWARD;
     constexpr uint32_t idesc = umma_idesc(TM, TN, a_m, b_n);
+    const uint32_t s0 = smem_addr(ring);
+    const uint64_t da0 = a_m ? umma_smem_desc(s0, 8192, 1024) : umma_smem_desc(s0, 16, 1024);
+    const uint64_t db0 = b_n ? umma_smem_desc(s0 + A_BYTES, 8192, 1024) : umma_smem_desc(s0 + A_BYTES, 16, 1024);
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    Walk walk(sh, a.dev_status);
+    Walk<false> walk(sh, a.dev_status);
     while (ok && walk.next()) {
       const Tile& tile = walk.tile;
+      const bool two = halves == 2 && tile.halves == 2;
       for (int k = 0; k < tile.steps; ++k) {
         const int part = F == WGRAD ? k % PART : k;
-        if (part == 0) {
-          if (!(ok = wait_or_abort(&sh->acc_empty[acc], acc_phase ^ 1, sh, a.dev_status))) break;
-        }
-        if (!(ok = wait_or_abort(&sh->full[stage], phase, sh, a.dev_status))) break;
+        const bool last = k + 1 == tile.steps || (F == WGRAD && part + 1 == PART);
+        if (part == 0 && !(ok = wait_thread(&sh->acc_empty[acc], acc_phase ^ 1, sh, a.dev_status))) break;
+        if (!(ok = wait_thread(&sh->full[stage], phase, sh, a.dev_status))) break;
         umma_fence_after();
-        if (lane == 0) {
-          const uint32_t sa = smem_addr(ring + stage * STAGE_BYTES), sb = sa + A_BYTES;
-          const uint64_t da = a_m ? umma_smem_desc(sa, 8192, 1024) : umma_smem_desc(sa, 16, 1024);
-          const uint64_t db = b_n ? umma_smem_desc(sb, 8192, 1024) : umma_smem_desc(sb, 16, 1024);
+        const uint64_t da = da0 + (uint32_t)stage * (stage_bytes >> 4), db = db0 + (uint32_t)stage * (stage_bytes >> 4);
 #pragma unroll
-          for (int i = 0; i < TK / 16; ++i)  // 16 elements on: 32 bytes along K, two groups of 8 lines otherwise
-            umma_bf16(tmem + acc * TN, da + (a_m ? i * 128 : i * 2), db + (b_n ? i * 128 : i * 2), idesc,
-                      part > 0 || i > 0);
-          umma_commit(&sh->empty[stage]);
+        for (int i = 0; i < TK / 16; ++i)  // 16 elements on: 32 bytes along K, two groups of 8 lines otherwise
+          umma_bf16(tmem + acc * TN, da + (a_m ? i * 128 : i * 2), db + (b_n ? i * 128 : i * 2), idesc,
+                    part > 0 || i > 0);
+        if (last) umma_commit(&sh->acc_full[acc]);
+        if (two) {
+          // the next accumulator, which may be the first of its round
+          if (part == 0) {
+            if (!(ok = wait_thread(&sh->acc_empty[acc ^ 1], acc_phase ^ 1 ^ acc, sh, a.dev_status))) break;
+            umma_fence_after();
+          }
+#pragma unroll
+          for (int i = 0; i < TK / 16; ++i)
+            umma_bf16(tmem + (acc ^ 1) * TN, da + (a_m ? i * 128 : i * 2),
+                      db + (B_BYTES >> 4) + (b_n ? i * 128 : i * 2), idesc, part > 0 || i > 0);
+          if (last) umma_commit(&sh->acc_full[acc ^ 1]);
         }
-        __syncwarp();
-        if (++stage == EXP_STAGES) {
+        umma_commit(&sh->empty[stage]);
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
-        if (k + 1 == tile.steps || (F == WGRAD && part + 1 == PART)) {
-          if (lane == 0) umma_commit(&sh->acc_full[acc]);
-          __syncwarp();
-          if (++acc == 2) {
-            acc = 0;
+        if (last) {  // on by the accumulators taken: two bring the same one around again
+          if (two)
             acc_phase ^= 1;
-          }
+          else if (++acc == 2)
+            acc = 0, acc_phase ^= 1;
         }
       }
     }
@@ -463,16 +527,18 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     int hint = 0, at = 0;
     uint32_t phase = 0;
     for (int t = first;; t += step) {
-      if (!wait_or_abort(&sh->tile_empty[at], phase ^ 1, sh, a.dev_status)) break;
+      if (!wait_warp(&sh->tile_empty[at], phase ^ 1, sh, a.dev_status)) break;
       Tile tile = {};
       tile.steps = -1;
-      if (t < total) tile = find_tile<F>(a, sh, t, &hint);
+      tile.halves = 1;
+      if (t < order.wide + order.narrow) tile = find_tile<F>(a, sh, order, t, &hint);
+      if (tile.halves == 0) continue;
       if (lane == 0) {
         sh->tiles[at] = tile;
         mbar_arrive(&sh->tile_full[at]);
       }
       __syncwarp();
-      if (t >= total) break;
+      if (tile.steps < 0) break;
       if (++at == TILES_AHEAD) {
         at = 0;
         phase ^= 1;
@@ -482,19 +548,19 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     // ---- zero the lines behind a slot's end in its last block of rows
     int block = 0;  // blocks of rows so far, modulo the stages
     uint32_t phases = 0;
-    Walk walk(sh, a.dev_status);
+    Walk<true> walk(sh, a.dev_status);
     while (walk.next()) {
       const Tile& tile = walk.tile;
-      block = (block + tile.steps) % EXP_STAGES;
+      block = (block + tile.steps) % stages;
       const int valid = tile.slot.len % TK;
       if (valid == 0) continue;
-      const int stage = (block + EXP_STAGES - 1) % EXP_STAGES;
-      if (!wait_or_abort(&sh->tail[stage], phases >> stage & 1, sh, a.dev_status)) break;
+      const int stage = (block + stages - 1) % stages;
+      if (!wait_warp(&sh->tail[stage], phases >> stage & 1, sh, a.dev_status)) break;
       phases ^= 1u << stage;
-      uint8_t* s = ring + stage * STAGE_BYTES;
+      uint8_t* s = ring + stage * stage_bytes;
       for (int i = lane; i < (TK - valid) * 8; i += 32) {
 #pragma unroll
-        for (int c = 0; c < (int)STAGE_BYTES / 8192; ++c)
+        for (int c = 0; c < (int)stage_bytes / 8192; ++c)
           *reinterpret_cast<uint4*>(s + c * 8192 + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -510,7 +576,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    Walk walk(sh, a.dev_status);
+    Walk<true> walk(sh, a.dev_status);
     while (ok && walk.next()) {
       const Tile& tile = walk.tile;
       const int m = tile.m + rank * (TM / 2) + row;
@@ -520,7 +586,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
         for (int i = 0; i < TN / 2; ++i) sum[i] = 0.f;
         for (int k = 0; k < tile.steps; k += PART) {
-          if (!(ok = wait_or_abort(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
+          if (!(ok = wait_warp(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
           umma_fence_after();
 #pragma unroll
           for (int c = 0; c < TN / 2; c += 16) {
@@ -545,59 +611,99 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
           if (n < a.N) store_grad(turn, a, tile.slot.w, (int64_t)m * a.N + n, sum + c, rows, a.N - n);
         }
       } else {
-        if (!(ok = wait_or_abort(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
-        umma_fence_after();
-        const uint32_t src = tmem + lanes + acc * TN + col;
         const int64_t at = tile.slot.begin + m;
-#pragma unroll 1
-        for (int c = 0; c < tn / 2; c += 32) {
-          const int n = tile.n + col + c;
-          if (rows <= 0 || n >= a.N) break;  // the same for the whole warp
-          uint32_t r[32], u[32];
-          tmem_load(src + c, r);
-          if (F == UP) tmem_load(src + TN / 2 + c, u);
-          float g[32], w[32];
-          if (F == UP_BACKWARD) {  // the loads run beside the accumulator's
-            load_rows(turn, g, a.gu + at * 2 * a.N + n, 2 * a.N, rows, a.N - n);
-            load_rows(turn, w, a.gu + at * 2 * a.N + a.N + n, 2 * a.N, rows, a.N - n);
+        for (int h = 0; ok && h < tile.halves; ++h) {
+          const int n = tile.n + h * tn + col;
+          const bool any = rows > 0 && n < a.N;  // the same for the whole warp
+          const uint32_t src = tmem + lanes + acc * TN + col;
+          const uint32_t free = leader_addr(&sh->acc_empty[acc]);
+          uint4 g[4], w[4];
+          if (F == UP_BACKWARD && any) {
+            fetch_rows(turn, g, a.gu + at * 2 * a.N + n, 2 * a.N, rows, a.N - n);
+            fetch_rows(turn, w, a.gu + at * 2 * a.N + a.N + n, 2 * a.N, rows, a.N - n);
           }
-          tmem_wait_load(r);
-          if (F == UP) tmem_wait_load(u);
-          float v[32];
+          if (!(ok = wait_warp(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
+          umma_fence_after();
+          if (!any) {
+            __syncwarp();
+            if (lane == 0) pair_arrive(free);
+          } else if (F == UP_BACKWARD) {
+            uint32_t v[2][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          if (F == Y_NT || F == Y_NN) {
-            store_rows(turn, v, a.y + at * a.N + n, a.N, rows, a.N - n);
-          } else if (F == UP) {
+            for (int c = 0; c < TN / 2; c += 32) {
+              if (c % 64 == 0) {
+                tmem_load(src + c, v[0]);
+                tmem_load(src + c + 32, v[1]);
+                tmem_wait_load(v[0]);
+                tmem_wait_load(v[1]);
+                if (c) {
+                  umma_fence_before();
+                  __syncwarp();
+                  if (lane == 0) pair_arrive(free);
+                }
+              }
+              uint4 qg[4], qw[4], qh[4];
+              turn_rows(turn, g, qg);
+              turn_rows(turn, w, qw);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __uint_as_float(u[i]);
-            if (a.y2) {
-              store_rows(turn, v, a.y2 + at * 2 * a.N + n, 2 * a.N, rows, a.N - n);
-              store_rows(turn, w, a.y2 + at * 2 * a.N + a.N + n, 2 * a.N, rows, a.N - n);
+              for (int i = 0; i < 4; ++i) {
+                float dg[8], du[8], h8[8];
+                unpack8(qg[i], dg);
+                unpack8(qw[i], du);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float dh = __uint_as_float(v[c / 32 % 2][8 * i + j]);
+                  const float sg = sigmoid_fast(dg[j]), si = dg[j] * sg;
+                  h8[j] = si * du[j];
+                  dg[j] = dh * du[j] * (sg + si * (1.f - sg));
+                  du[j] = dh * si;
+                }
+                qg[i] = pack8(dg);
+                qw[i] = pack8(du);
+                qh[i] = pack8(h8);
+              }
+              const int nc = n + c;
+              if (c + 32 < TN / 2) {
+                fetch_rows(turn, g, a.gu + at * 2 * a.N + nc + 32, 2 * a.N, rows, a.N - nc - 32);
+                fetch_rows(turn, w, a.gu + at * 2 * a.N + a.N + nc + 32, 2 * a.N, rows, a.N - nc - 32);
+              }
+              store_rows(turn, qg, a.y + at * 2 * a.N + nc, 2 * a.N, rows, a.N - nc);
+              store_rows(turn, qw, a.y + at * 2 * a.N + a.N + nc, 2 * a.N, rows, a.N - nc);
+              if (a.y2) store_rows(turn, qh, a.y2 + at * a.N + nc, a.N, rows, a.N - nc);
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid_fast(v[i]) * w[i];
-            store_rows(turn, v, a.y + at * a.N + n, a.N, rows, a.N - n);
           } else {
-            float h[32];
+            // all of it into registers first: the products wait for the accumulator, not for the stores
+            uint32_t v[4][32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float sg = sigmoid_fast(g[i]), si = g[i] * sg;
-              h[i] = si * w[i];
-              g[i] = v[i] * w[i] * (sg + si * (1.f - sg));
-              w[i] = v[i] * si;
+            for (int c = 0; c < 4; ++c)  // UP: the gate's 64 columns, then the up projection's
+              tmem_load(src + (F == UP && c >= 2 ? TN / 2 + (c - 2) * 32 : c * 32), v[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait_load(v[c]);
+            umma_fence_before();
+            __syncwarp();
+            if (lane == 0) pair_arrive(free);
+#pragma unroll
+            for (int c = 0; c < tn / 2; c += 32) {
+              const int nc = n + c;
+              float* x = reinterpret_cast<float*>(v[c / 32]);
+              if (F != UP) {
+                store_rows(turn, x, a.y + at * a.N + nc, a.N, rows, a.N - nc);
+              } else {
+                float* u = reinterpret_cast<float*>(v[c / 32 + 2]);
+                if (a.y2) {
+                  store_rows(turn, x, a.y2 + at * 2 * a.N + nc, 2 * a.N, rows, a.N - nc);
+                  store_rows(turn, u, a.y2 + at * 2 * a.N + a.N + nc, 2 * a.N, rows, a.N - nc);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = x[i] * sigmoid_fast(x[i]) * u[i];
+                store_rows(turn, x, a.y + at * a.N + nc, a.N, rows, a.N - nc);
+              }
             }
-            store_rows(turn, g, a.y + at * 2 * a.N + n, 2 * a.N, rows, a.N - n);
-            store_rows(turn, w, a.y + at * 2 * a.N + a.N + n, 2 * a.N, rows, a.N - n);
-            if (a.y2) store_rows(turn, h, a.y2 + at * a.N + n, a.N, rows, a.N - n);
           }
-        }
-        umma_fence_before();
-        __syncwarp();
-        if (lane == 0) pair_arrive(leader_addr(&sh->acc_empty[acc]));
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1;
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1;
+          }
         }
       }
     }
@@ -617,7 +723,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
   if (warp == 2) tmem_free(tmem, 2 * TN);
 }
 
-constexpr size_t EXP_SMEM = 1024 + EXP_STAGES * STAGE_BYTES + sizeof(ExpertShared);
+constexpr size_t EXP_SMEM = 1024 + RING_BYTES + sizeof(ExpertShared);
 
 template <Form F>
 static int launch_experts(const CUtensorMap& ma, const CUtensorMap& mb, const ExpertArgs& a, cudaStream_t stream) {
