@@ -27,6 +27,7 @@
  *   ep_expert_up, ep_expert_gemm, ep_expert_up_backward, ep_expert_wgrad (the
  *       experts' products over the slots of the dispatch buffer, and their
  *       gradients)
+ *   ep_adamw (an optimizer step over many tensors, from the reduced gradients)
  *
  * Sources, cited by page title and section:
  *  [GR] "MoonEP: πώς η εξισορρόπηση των AI experts αλλάζει την υποδομή των MoE
@@ -742,6 +743,49 @@ EP_API int ep_expert_wgrad(const uint16_t* a, const uint16_t* b, int64_t rows, i
                            const int32_t* cu_seqlens, int n_slots, const int32_t* slot_order, float* g_home,
                            int n_home, int64_t ld_home, void* g_rep, int rep_dtype, int n_rep, int64_t ld_rep,
                            int accumulate, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * One AdamW step over many tensors at once.  With t = *step (1 in the first
+ * step; the caller counts), lr = *lr_dev if given, g scaled by *grad_scale if
+ * given, every operation rounded to fp32 by itself:
+ *   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) (g g)
+ *   p = p (1 - lr wd) - (m lr / (1 - b1^t)) / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * with the factors of lr, wd, b1^t and b2^t computed in fp64 and rounded once.
+ *   state_bits 32: m and v fp32 [n].
+ *   state_bits 8:  m and v are e4m3 codes [n] with one fp32 scale for each block
+ *     of EP_ADAMW_BLOCK elements (m_scale, v_scale [ceil(n / EP_ADAMW_BLOCK)]):
+ *     m = code * scale, and v = (code * scale)^2: the second moment is held as
+ *     its root.  scale = largest * (1 / 448), largest the block's largest magnitude;
+ *     codes are value * (448 * (1 / largest)) rounded to nearest even; a nonzero
+ *     root gets at least the smallest code; a block with no magnitude above 2^-100
+ *     is held as zeros.
+ *     p is computed before the moments are coded.  Zeroed codes and scales are a
+ *     fresh state.  A NaN keeps to its element; an infinity takes its block along.
+ * All pointers of a tensor are device pointers of its own; t.p, t.m, t.v, the
+ * scales and t.copy are updated in place.  Tensors may have any length (0 too)
+ * and any alignment that fits their elements; 16-byte aligned ones are faster.
+ * The table is host memory and is read before the call returns; one launch takes
+ * up to 256 tensors.  `step`, `lr_dev` and `grad_scale` are read by the kernel, so a
+ * captured call replays with their current values.
+ */
+#define EP_ADAMW_BLOCK 256
+
+typedef struct {
+  float* p;        /* [n] parameters, fp32 */
+  const void* g;   /* [n] gradient, fp32 or bf16 (grad_dtype) */
+  void* m;         /* [n] first moment */
+  void* v;         /* [n] second moment, or the codes of its root */
+  float* m_scale;  /* state_bits 8 only */
+  float* v_scale;
+  uint16_t* copy;  /* [n] p rounded to bf16, out, or NULL */
+  int64_t n;
+  int64_t vec;     /* not read: set inside the library */
+} EpAdamWTensor;
+
+EP_API int ep_adamw(const EpAdamWTensor* tensors /* host */, int n_tensors, int state_bits, int grad_dtype,
+                    const int32_t* step, double lr, const float* lr_dev, double beta1, double beta2, double eps,
+                    double weight_decay, const float* grad_scale, cudaStream_t stream);
 
 /*
  * Self-test of failure detection (no counterpart on the pages): runs

@@ -56,6 +56,13 @@ class EpQuotaLayout(ctypes.Structure):
                                       "cu_seqlens")]
 
 
+class EpAdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "m", "v", "m_scale", "v_scale", "copy")] + [
+        ("n", ctypes.c_int64), ("vec", ctypes.c_int64)]
+
+
+EP_ADAMW_BLOCK = 256
+
 _lib = None
 _V, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 _F, _D = ctypes.c_float, ctypes.c_double
@@ -103,6 +110,7 @@ _SIGS = {
     "ep_expert_up": (_I, [_V, _I64, _I64, _V, _I, _I64, _V, _I, _V, _V, _I, _V, _V, _V, _V]),
     "ep_expert_up_backward": (_I, [_V, _I64, _I64, _V, _I, _I64, _V, _V, _I, _V, _V, _I, _V, _V, _V, _V]),
     "ep_expert_wgrad": (_I, [_V, _V, _I64, _I64, _I64, _V, _I, _V, _V, _I, _I64, _V, _I, _I, _I64, _I, _V, _V]),
+    "ep_adamw": (_I, [_V, _I, _I, _I, _V, _D, _V, _D, _D, _D, _D, _V, _V]),
     "ep_status_read": (_I, [_V, _V, _V]),
     "ep_selftest_lookback_timeout": (_I, [_V, _I64, _I, _I, _V, _V, _V, _SZ, _V, _V]),
 }
@@ -696,6 +704,62 @@ def ep_expert_wgrad(a, b, cu_seqlens, g_home, g_rep=None, accumulate=False, slot
         _check("ep_expert_wgrad",
                lib().ep_expert_wgrad(_p(a), _p(b), rows, M, N, cu, n, order, home, g_home.shape[0], ld_home, rep, dt,
                                      n_rep, ld_rep, int(bool(accumulate)), _p(dev_status), _s(stream)))
+
+
+def adamw_table(params, grads, m, v, m_scale=None, v_scale=None, copies=None):
+    """The host table of ep_adamw for lists of tensors (one entry each): fp32
+    params, fp32 or bf16 grads, moments in fp32 or as float8_e4m3fn codes with
+    their fp32 block scales, bf16 copies or None.  Returns (table, state_bits,
+    grad_dtype).  It holds addresses: keep the tensors as long as it is used."""
+    k = len(params)
+    eight = m_scale is not None
+    for name, ts in (("grads", grads), ("m", m), ("v", v), ("m_scale", m_scale), ("v_scale", v_scale),
+                     ("copies", copies)):
+        if ts is not None and len(ts) != k:
+            raise ValueError(f"{len(ts)} {name} for {k} params")
+    if eight != (v_scale is not None):
+        raise ValueError("m_scale and v_scale go together")
+    gdt = {g.dtype for g in grads}
+    if not gdt <= {torch.float32, torch.bfloat16} or len(gdt) > 1:
+        raise TypeError(f"gradients of {gdt}, expected all fp32 or all bf16")
+    state = torch.float8_e4m3fn if eight else torch.float32
+    table = (EpAdamWTensor * max(1, k))()
+    for i, p in enumerate(params):
+        n = p.numel()
+        row = dict(p=(p, torch.float32, n), g=(grads[i], grads[i].dtype, n), m=(m[i], state, n), v=(v[i], state, n))
+        if eight:
+            blocks = -(-n // EP_ADAMW_BLOCK)
+            row.update(m_scale=(m_scale[i], torch.float32, blocks), v_scale=(v_scale[i], torch.float32, blocks))
+        if copies is not None and copies[i] is not None:
+            row.update(copy=(copies[i], torch.bfloat16, n))
+        for field, (t, dt, count) in row.items():
+            _dtype(t, dt)
+            if t.numel() != count:
+                raise ValueError(f"{field} of tensor {i}: {t.numel()} elements, expected {count}")
+            if t.device != params[0].device:
+                raise ValueError(f"tensors on {params[0].device} and {t.device}")
+            setattr(table[i], field, _p(t).value)
+        table[i].n = n
+    return table, 8 if eight else 32, EP_DTYPE_BF16 if gdt == {torch.bfloat16} else EP_DTYPE_F32
+
+
+def ep_adamw(table, n_tensors, state_bits, grad_dtype, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
+             grad_scale=None, stream=None):
+    """One AdamW step over the tensors of an adamw_table, in place.  step: int32
+    tensor [1], 1 in the first step; lr: a number or an fp32 tensor [1];
+    grad_scale: fp32 tensor [1] that multiplies the gradients, or None."""
+    _dtype(step, torch.int32)
+    lr_dev = lr if isinstance(lr, torch.Tensor) else None
+    for t in (lr_dev, grad_scale):
+        if t is not None:
+            _dtype(t, torch.float32)
+    for name, t in (("step", step), ("lr", lr_dev), ("grad_scale", grad_scale)):
+        if t is not None and t.numel() != 1:
+            raise ValueError(f"{name}: expected one element")
+    with _device_of(step, lr_dev, grad_scale):
+        _check("ep_adamw", lib().ep_adamw(table, n_tensors, state_bits, grad_dtype, _p(step),
+                                          0.0 if lr_dev is not None else lr, _p(lr_dev), betas[0], betas[1], eps,
+                                          weight_decay, _p(grad_scale), _s(stream)))
 
 
 def ep_selftest_lookback_timeout(topk_ids, E, loads, max_vio, ws, dev_status, stream=None):

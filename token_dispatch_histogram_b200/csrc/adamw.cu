@@ -1,0 +1,293 @@
+// One AdamW step over many tensors at once, behind the replica gradient
+// reduction: element by element, with g the gradient (scaled), t the step,
+//   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - (m lr / (1 - b1^t)) / (sqrt(v) / sqrt(1 - b2^t) + eps)
+// and optionally the bf16 copy of p that the experts' products read.
+//
+// The moments are fp32, or 8 bits in blocks of 256 elements with one fp32 scale
+// each: e4m3 codes, the block's largest magnitude at 448.  The second moment is
+// held as its root (its range is that of |g| then), and a nonzero root never at
+// code 0, which a later step would divide by.  A step computes with the moments
+// before they are coded again.
+//
+// Every product, sum, quotient and root is rounded by itself, in the order
+// above, so the codes do not depend on how a compiler joins operations.
+//
+// Bound by memory: 28 bytes an element with fp32 moments, 16 with 8 bits, 2 more
+// for the copy.  A block of 256 elements belongs to one warp, eight consecutive
+// elements to a lane, so a lane's codes are 8 bytes and a block's maximum is a
+// shuffle reduction; nothing is shared between warps.
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "common.cuh"
+
+namespace ep {
+
+constexpr int ADAM_BLOCK = EP_ADAMW_BLOCK;
+constexpr int ADAM_WARPS = 8;
+constexpr int ADAM_TENSORS = 256;  // of one launch: the table is a kernel parameter
+constexpr float FP8_MAX = 448.f, FP8_MIN = 0x1p-9f, FP8_TINY = 0x1p-100f;
+
+struct AdamTable {
+  EpAdamWTensor t[ADAM_TENSORS];
+  int32_t before[ADAM_TENSORS + 1];  // blocks of 256 elements before each tensor
+  int n;
+};
+
+struct AdamArgs {
+  double lr, b1, b2, eps, wd;
+  const float* lr_dev;
+  const float* grad_scale;
+  const int32_t* step;
+};
+
+// What the elements need of the step, in fp32: computed once per CTA in fp64.
+struct AdamConst {
+  float b1, b2, c1m, c2m, decay, c1, c2, eps, gs;
+};
+
+__device__ __forceinline__ AdamConst adam_const(const AdamArgs& a) {
+  const double t = *a.step, lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
+  AdamConst c;
+  c.b1 = (float)a.b1;
+  c.b2 = (float)a.b2;
+  c.c1m = (float)(1.0 - a.b1);
+  c.c2m = (float)(1.0 - a.b2);
+  c.decay = (float)(1.0 - lr * a.wd);
+  c.c1 = (float)(lr / (1.0 - pow(a.b1, t)));
+  c.c2 = (float)(1.0 / sqrt(1.0 - pow(a.b2, t)));
+  c.eps = (float)a.eps;
+  c.gs = a.grad_scale ? *a.grad_scale : 1.f;
+  return c;
+}
+
+__device__ __forceinline__ void adam_element(const AdamConst& c, bool scaled, float& p, float g, float& m, float& v,
+                                             float& root) {
+  if (scaled) g = __fmul_rn(g, c.gs);
+  m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.c1m));
+  v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.c2m));
+  root = __fsqrt_rn(v);
+  p = __fsub_rn(__fmul_rn(p, c.decay),
+                __fdiv_rn(__fmul_rn(m, c.c1), __fadd_rn(__fmul_rn(root, c.c2), c.eps)));
+}
+
+// Eight consecutive elements from i on, those below n; whole and aligned ones as two 16-byte accesses.
+__device__ __forceinline__ void load8(const float* p, int64_t i, int64_t n, bool vec, float* x) {
+  if (vec && i + 8 <= n) {
+    const float4 a = *reinterpret_cast<const float4*>(p + i), b = *reinterpret_cast<const float4*>(p + i + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = i + j < n ? p[i + j] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store8(float* p, int64_t i, int64_t n, bool vec, const float* x) {
+  if (vec && i + 8 <= n) {
+    *reinterpret_cast<float4*>(p + i) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + i + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) p[i + j] = x[j];
+  }
+}
+
+__device__ __forceinline__ void load8_bf16(const uint16_t* p, int64_t i, int64_t n, bool vec, float* x) {
+  if (vec && i + 8 <= n) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p + i);
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = bf16_bits_to_f32(u[j] & 0xffffu);
+      x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = i + j < n ? bf16_bits_to_f32(p[i + j]) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store8_bf16(uint16_t* p, int64_t i, int64_t n, bool vec, const float* x) {
+  const uint32_t u[4] = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
+                         f32x2_to_bf16x2(x[6], x[7])};
+  if (vec && i + 8 <= n) {
+    *reinterpret_cast<uint4*>(p + i) = make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) p[i + j] = (uint16_t)(u[j >> 1] >> (j & 1) * 16);
+  }
+}
+
+__device__ __forceinline__ void load8_codes(const uint8_t* p, int64_t i, int64_t n, bool vec, float scale, float* x) {
+  uint32_t w[2] = {0, 0};
+  if (vec && i + 8 <= n) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p + i);
+    w[0] = q.x, w[1] = q.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) w[j >> 2] |= (uint32_t)p[i + j] << (j & 3) * 8;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // two codes to two halves, exactly
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (j & 1) * 16), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    x[2 * j] = __fmul_rn(f.x, scale);
+    x[2 * j + 1] = __fmul_rn(f.y, scale);
+  }
+}
+
+// Codes of a block's eight values a lane, and the block's scale (the same on every lane).
+template <bool ROOT>
+__device__ __forceinline__ float store8_codes(uint8_t* p, int64_t i, int64_t n, bool vec, const float* x) {
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));  // a NaN keeps to its own element
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const bool held = top > FP8_TINY;  // a block with nothing above that is held as zeros
+  const float inv = held ? __fmul_rn(__frcp_rn(top), FP8_MAX) : 0.f;
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    float y[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      y[k] = __fmul_rn(x[j + k], inv);
+      if (ROOT && x[j + k] > 0.f && y[k] < FP8_MIN) y[k] = FP8_MIN;
+    }
+    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    w[j >> 2] |= held ? c << (j & 2) * 8 : 0u;
+  }
+  if (vec && i + 8 <= n) {
+    *reinterpret_cast<uint2*>(p + i) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) p[i + j] = (uint8_t)(w[j >> 2] >> (j & 3) * 8);
+  }
+  return held ? __fmul_rn(top, 1.f / FP8_MAX) : 0.f;
+}
+
+template <bool EIGHT, bool GRAD_BF16>
+__global__ void __launch_bounds__(ADAM_WARPS * 32)
+    k_adamw(const __grid_constant__ AdamTable tab, const __grid_constant__ AdamArgs a) {
+  __shared__ AdamConst s_c;
+  if (threadIdx.x == 0) s_c = adam_const(a);
+  __syncthreads();
+  const AdamConst c = s_c;
+  const bool scaled = a.grad_scale != nullptr;
+  const int lane = threadIdx.x & 31;
+  const int total = tab.before[tab.n];
+  int k = 0;  // the tensor of the block at hand; blocks come in ascending order
+  for (int b = blockIdx.x * ADAM_WARPS + (threadIdx.x >> 5); b < total; b += gridDim.x * ADAM_WARPS) {
+    int hi = tab.n - 1;
+    if (tab.before[k + 1] > b) hi = k;
+    while (k < hi) {  // the last tensor with before <= b; those without elements have no blocks
+      const int mid = (k + hi + 1) >> 1;
+      if (tab.before[mid] <= b)
+        k = mid;
+      else
+        hi = mid - 1;
+    }
+    const EpAdamWTensor& t = tab.t[k];
+    const int64_t block = b - tab.before[k], i = block * ADAM_BLOCK + lane * 8, n = t.n;
+    const bool vec = t.vec != 0;
+    float p[8], g[8], m[8], v[8], root[8];
+    load8((const float*)t.p, i, n, vec, p);
+    if (GRAD_BF16)
+      load8_bf16((const uint16_t*)t.g, i, n, vec, g);
+    else
+      load8((const float*)t.g, i, n, vec, g);
+    if (EIGHT) {
+      load8_codes((const uint8_t*)t.m, i, n, vec, t.m_scale[block], m);
+      load8_codes((const uint8_t*)t.v, i, n, vec, t.v_scale[block], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+    } else {
+      load8((const float*)t.m, i, n, vec, m);
+      load8((const float*)t.v, i, n, vec, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) adam_element(c, scaled, p[j], g[j], m[j], v[j], root[j]);
+    store8((float*)t.p, i, n, vec, p);
+    if (t.copy) store8_bf16((uint16_t*)t.copy, i, n, vec, p);
+    if (EIGHT) {
+      // elements behind the tensor's end are 0 all along, and a 0 gradient keeps them so
+      const float ms = store8_codes<false>((uint8_t*)t.m, i, n, vec, m);
+      const float vs = store8_codes<true>((uint8_t*)t.v, i, n, vec, root);
+      if (lane == 0) {
+        t.m_scale[block] = ms;
+        t.v_scale[block] = vs;
+      }
+    } else {
+      store8((float*)t.m, i, n, vec, m);
+      store8((float*)t.v, i, n, vec, v);
+    }
+  }
+}
+
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_adamw(const EpAdamWTensor* tensors, int n_tensors, int state_bits, int grad_dtype,
+                        const int32_t* step, double lr, const float* lr_dev, double beta1, double beta2, double eps,
+                        double weight_decay, const float* grad_scale, cudaStream_t stream) {
+  if (n_tensors < 0 || (state_bits != 8 && state_bits != 32)) return EP_ERR_ARG;
+  if (grad_dtype != EP_DTYPE_F32 && grad_dtype != EP_DTYPE_BF16) return EP_ERR_ARG;
+  if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && eps >= 0.0) || !isfinite(eps) || !isfinite(lr) ||
+      !isfinite(weight_decay))
+    return EP_ERR_ARG;
+  if (n_tensors == 0) return EP_OK;
+  if (!tensors || !step || ((uintptr_t)step & 3) || ((uintptr_t)lr_dev & 3) || ((uintptr_t)grad_scale & 3))
+    return EP_ERR_ARG;
+  const bool eight = state_bits == 8, gb = grad_dtype == EP_DTYPE_BF16;
+  const uintptr_t gmask = gb ? 1 : 3, smask = eight ? 0 : 3;
+  for (int i = 0; i < n_tensors; ++i) {
+    const EpAdamWTensor& t = tensors[i];
+    if (t.n < 0 || (t.n + ADAM_BLOCK - 1) / ADAM_BLOCK >= ((int64_t)1 << 30)) return EP_ERR_ARG;
+    if (t.n == 0) continue;
+    if (!t.p || !t.g || !t.m || !t.v || (eight && (!t.m_scale || !t.v_scale))) return EP_ERR_ARG;
+    if (((uintptr_t)t.p & 3) || ((uintptr_t)t.g & gmask) || ((uintptr_t)t.m & smask) || ((uintptr_t)t.v & smask) ||
+        ((uintptr_t)t.copy & 1) || ((uintptr_t)t.m_scale & 3) || ((uintptr_t)t.v_scale & 3))
+      return EP_ERR_ARG;
+  }
+  const AdamArgs a{lr, beta1, beta2, eps, weight_decay, lr_dev, grad_scale, step};
+  AdamTable tab;
+  int i = 0;
+  while (i < n_tensors) {
+    tab.n = 0;
+    int64_t blocks = 0;
+    for (; i < n_tensors && tab.n < ADAM_TENSORS; ++i) {
+      EpAdamWTensor t = tensors[i];
+      if (t.n == 0) continue;
+      const int64_t more = (t.n + ADAM_BLOCK - 1) / ADAM_BLOCK;
+      if (blocks + more >= ((int64_t)1 << 30)) break;
+      t.vec = aligned16(t.p) && aligned16(t.g) && aligned16(t.copy) && aligned16(t.m) && aligned16(t.v);
+      tab.before[tab.n] = (int32_t)blocks;
+      tab.t[tab.n++] = t;
+      blocks += more;
+    }
+    if (tab.n == 0) break;
+    tab.before[tab.n] = (int32_t)blocks;
+    const int64_t want = (blocks + ADAM_WARPS - 1) / ADAM_WARPS, most = (int64_t)num_sms() * 8;
+    const unsigned grid = (unsigned)(want < most ? want : most);
+    if (eight && gb)
+      k_adamw<true, true><<<grid, ADAM_WARPS * 32, 0, stream>>>(tab, a);
+    else if (eight)
+      k_adamw<true, false><<<grid, ADAM_WARPS * 32, 0, stream>>>(tab, a);
+    else if (gb)
+      k_adamw<false, true><<<grid, ADAM_WARPS * 32, 0, stream>>>(tab, a);
+    else
+      k_adamw<false, false><<<grid, ADAM_WARPS * 32, 0, stream>>>(tab, a);
+    count_launch();
+    const int rc = launch_status();
+    if (rc != EP_OK) return rc;
+  }
+  return EP_OK;
+}
