@@ -89,6 +89,8 @@ struct RouterArgs {
   int E, K, n_group, topk_group, group_top;
   bool sigmoid, renorm;
   float scale;
+  int lanes_per_group;  // 32 / n_group, n_group rounded up to a power of two
+  uint32_t group_inv;   // e * group_inv >> 21 == e / (E / n_group) for e < 1024
 };
 
 // One token by one warp, everything that decides held in 64 bits; key: E doubles
@@ -182,41 +184,233 @@ __device__ int select_exact(const RouterArgs& a, const V* __restrict__ row, cons
   return mine;
 }
 
-template <typename V>
-__global__ void __launch_bounds__(ROUTER_WARPS * 32)
-    k_router(const V* __restrict__ logits, const float* __restrict__ bias, RouterArgs a, int32_t* __restrict__ ids,
-             float* __restrict__ w, int32_t* dev_status) {
-  extern __shared__ double s_key[];  // [warps][E]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + warp;
-  if (t >= a.T) return;
-  const V* row = logits + t * a.ld;
-  bool bad = false;
-  for (int e = lane; e < a.E; e += 32) clean_logit(to_f32(row[e]), bad);
-  const int id = select_exact(a, row, bias, s_key + (size_t)warp * a.E);
-  bool ignore = false;
-  const float x = lane < a.K ? clean_logit(to_f32(row[id]), ignore) : -INFINITY;
-  float v;
-  if (a.renorm) {
-    v = chosen_ratio(x, a.sigmoid);
-  } else if (a.sigmoid) {
-    v = sigmoid_f32(x);
-  } else {
-    float m = -INFINITY, z = 0.f;
-    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, clean_logit(to_f32(row[e]), ignore));
-    m = warp_max(m);
-    if (m == -INFINITY) {
-      v = 0.f;
-    } else {
-      for (int e = lane; e < a.E; e += 32) z += expf(clean_logit(to_f32(row[e]), ignore) - m);
-      v = expf(x - m) / warp_sum(z);
+__device__ __forceinline__ float warp_fmax(float v) {  // NaN on a lane counts as nothing
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Bounds of what the fast path's keys are off, from its steps: e^-x by ex2 of a
+// rounded product (|x| 2^-24 and 2^-22 of itself), a sum, a quotient (2^-22), the
+// bias added (2^-24 of the key).  Sigmoid: s (1 - s) |x| <= 0.23, so below 5e-7 of
+// 1.  Softmax: a sum of up to 1024 terms besides (37 roundings of 2^-24), so below
+// 4e-6 of s, and t e^-t <= 0.37 of 2^-23 for its own exponent.
+__device__ __forceinline__ float key_error(bool sigmoid, float s, float key) {
+  return (sigmoid ? 5e-7f : 1e-7f + 4e-6f * s) + 1.2e-7f * fabsf(key);
+}
+
+struct Candidate {
+  float key;
+  int e;
+};
+
+constexpr int HOISTED = 16;  // logits a lane up to which its biases stay in registers
+
+// Lists of a warp: up to 64 candidates, then the first K + 1 in order.
+struct RouterList {
+  Candidate c[64];
+  Candidate sorted[33];
+};
+
+__device__ __forceinline__ bool goes_before(const Candidate& a, const Candidate& b) {
+  return a.key > b.key || (a.key == b.key && a.e < b.e);
+}
+
+// The groups to take from, as a mask over groups, from the values at row[0, E) in
+// shared memory; false when two groups at the border are too close to tell.
+// 32 / n lanes (n the next power of two) share a group and go through it from
+// different places, so that groups a multiple of 32 apart use different banks.
+__device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* row, bool approximate, uint32_t* keep) {
+  const int lane = threadIdx.x & 31, len = a.E / a.n_group;
+  const int per = a.lanes_per_group, g = lane / per, s = lane % per, turns = (len + per - 1) / per;
+  float first = -INFINITY, second = -INFINITY;
+  if (g < a.n_group) {
+    int r = g % turns;
+    for (int i = 0; i < turns; ++i) {
+      const int at = s + per * r;
+      const float v = at < len ? row[g * len + at] : -INFINITY;
+      second = fmaxf(second, fminf(first, v));
+      first = fmaxf(first, v);
+      if (++r == turns) r = 0;
     }
   }
-  if (lane < a.K) {
-    ids[t * a.K + lane] = id;
-    w[t * a.K + lane] = a.scale * v;
+  for (int d = 1; d < per; d <<= 1) {
+    const float f = __shfl_xor_sync(0xffffffffu, first, d), o = __shfl_xor_sync(0xffffffffu, second, d);
+    second = fmaxf(fminf(first, f), fmaxf(second, o));
+    first = fmaxf(first, f);
   }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) flag(dev_status, EP_DEV_BAD_LOGIT);
+  float score = first;
+  if (a.group_top == 2 && second != -INFINITY) score += second;
+  // of two keys: twice the error of one, and the sum's rounding; s is at most 1
+  const float near = approximate ? 4.f * key_error(a.sigmoid, 1.f, 0.f) + 6e-7f * fabsf(score) : 0.f;
+  int before = 0;
+  uint32_t close = 0;
+  for (int i = 0; i < a.n_group; ++i) {
+    const float o = __shfl_sync(0xffffffffu, score, i * per);
+    before += o > score || (o == score && i < g);
+    if (approximate && fabsf(o - score) <= near) close |= 1u << i;
+  }
+  const bool mine = g < a.n_group && before < a.topk_group;
+  uint32_t k = __ballot_sync(0xffffffffu, mine && s == 0), m = 0;
+  for (int i = 0; i < a.n_group; ++i) m |= (k >> (i * per) & 1u) << i;
+  *keep = m;
+  const bool tight = g < a.n_group && (close & (mine ? ~m : m)) != 0;
+  return !__any_sync(0xffffffffu, tight);
+}
+
+// One token by one warp in fp32, NV logits a lane.  Lane k < K returns the k-th
+// expert, or every lane -1 where fp32 cannot tell: the caller then takes
+// select_exact.  The K + 1 largest are among the elements that reach the
+// (K + 1)-th largest of the lanes' own maxima: usually few more than K + 1, which
+// are ranked against each other.
+template <typename V, int NV>
+__device__ __forceinline__ int select_fast(const RouterArgs& a, const V* __restrict__ logits, const float (&x)[NV],
+                                           const float (&b)[NV], const float* __restrict__ bias, RouterList* list,
+                                           float* row, float* top_logit, float* total) {
+  const int lane = threadIdx.x & 31;
+  const bool group_scores = a.n_group > 1 && !bias && a.group_top == 2;
+  const bool scores = bias != nullptr || group_scores;
+  float key[NV];
+  float m = -INFINITY, z = 0.f;
+  if (!a.sigmoid && (scores || !a.renorm)) {  // softmax over the row
+#pragma unroll
+    for (int j = 0; j < NV; ++j) m = fmaxf(m, x[j]);
+    m = warp_fmax(m);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      key[j] = m == -INFINITY ? 0.f : __expf(x[j] - m);
+      z += lane + 32 * j < a.E ? key[j] : 0.f;
+    }
+    z = warp_sum(z);
+  }
+  *top_logit = m;
+  *total = z;
+  if (scores) {
+    const float iz = z > 0.f ? __fdividef(1.f, z) : 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      key[j] = a.sigmoid ? __fdividef(1.f, 1.f + __expf(-x[j])) : key[j] * iz;
+      if (bias) key[j] += NV <= HOISTED ? b[j] : lane + 32 * j < a.E ? bias[lane + 32 * j] : 0.f;
+      if (x[j] == -INFINITY) key[j] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) key[j] = x[j];
+  }
+  uint32_t keep = 0xffffffffu;
+  if (a.n_group > 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (lane + 32 * j < a.E) row[lane + 32 * j] = key[j];
+    __syncwarp();
+    if (!keep_groups(a, row, scores, &keep)) return -1;
+    if (group_scores) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] = x[j];
+    }
+  }
+  // NaN: not there (past E, or of a group left out)
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e = lane + 32 * j;
+    const uint32_t g = (uint32_t)e * a.group_inv >> 21;
+    if (e >= a.E || (a.n_group > 1 && !(keep >> g & 1))) key[j] = NAN;
+  }
+  float own = NAN;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) own = fmaxf(own, key[j]);
+  float t = NAN;
+  for (int k = 0; k <= a.K; ++k) {
+    t = warp_fmax(own);
+    if (own == t) own = NAN;
+  }
+  if (isnan(t)) t = -INFINITY;
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) mine += key[j] >= t;
+  int n = 0, at = 0;
+  for (int i = 1;; ++i) {
+    const uint32_t have = __ballot_sync(0xffffffffu, mine >= i);
+    if (!have) break;
+    at += __popc(have & lanemask_lt());
+    n += __popc(have);
+  }
+  if (n > 64) return -1;
+  // at: the lower lanes' candidates (those that have an i-th, summed over i), and so this lane's first place
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (key[j] >= t) list->c[at++] = Candidate{key[j], lane + 32 * j};
+  __syncwarp();
+  const Candidate none{NAN, INT_MAX};
+  const Candidate c0 = lane < n ? list->c[lane] : none, c1 = lane + 32 < n ? list->c[lane + 32] : none;
+  int r0 = 0, r1 = 0;
+  for (int i = 0; i < n; ++i) {
+    const Candidate o = list->c[i];
+    r0 += goes_before(o, c0);
+    if (n > 32) r1 += goes_before(o, c1);
+  }
+  if (lane < n && r0 <= a.K) list->sorted[r0] = c0;
+  if (lane + 32 < n && r1 <= a.K) list->sorted[r1] = c1;
+  __syncwarp();
+  const int have = min(n, a.K + 1);
+  const Candidate c = lane < have ? list->sorted[lane] : none;
+  bool tight = false;
+  if (bias) {
+    const Candidate o = lane + 1 < have ? list->sorted[lane + 1] : none;
+    if (lane < a.K && o.e != INT_MAX && o.key != -INFINITY) {
+      const float bc = bias[c.e], bo = bias[o.e];
+      tight = c.key - o.key <= key_error(a.sigmoid, c.key - bc, c.key) + key_error(a.sigmoid, o.key - bo, o.key);
+      if (tight && bc == bo) tight = to_f32(logits[c.e]) != to_f32(logits[o.e]);  // equal in truth: in order as it is
+    }
+  }
+  __syncwarp();
+  return __any_sync(0xffffffffu, tight) ? -1 : c.e;
+}
+
+template <typename V, int NV>
+__global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3 : 2)
+    k_router(const V* __restrict__ logits, const float* __restrict__ bias, RouterArgs a, int32_t* __restrict__ ids,
+             float* __restrict__ w, int32_t* dev_status) {
+  extern __shared__ double s_key[];  // [warps][E], of select_exact (select_fast uses it as fp32)
+  __shared__ RouterList s_list[ROUTER_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double* mine = s_key + (size_t)warp * a.E;
+  float b[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) b[j] = NV <= HOISTED && bias && lane + 32 * j < a.E ? bias[lane + 32 * j] : 0.f;
+  for (int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + warp; t < a.T; t += (int64_t)gridDim.x * ROUTER_WARPS) {
+    const V* row = logits + t * a.ld;
+    float x[NV];
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) x[j] = lane + 32 * j < a.E ? to_f32(row[lane + 32 * j]) : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) bad |= !(x[j] <= FLT_MAX);
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad) {
+      bool ignore = false;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) x[j] = clean_logit(x[j], ignore);
+      if (lane == 0) flag(dev_status, EP_DEV_BAD_LOGIT);
+    }
+    float m, z;
+    int id = select_fast<V, NV>(a, row, x, b, bias, s_list + warp, reinterpret_cast<float*>(mine), &m, &z);
+    if (__any_sync(0xffffffffu, id < 0)) id = select_exact(a, row, bias, mine);
+    bool ignore = false;
+    const float xs = lane < a.K ? clean_logit(to_f32(row[id]), ignore) : -INFINITY;
+    float v;
+    if (a.renorm)
+      v = chosen_ratio(xs, a.sigmoid);
+    else if (a.sigmoid)
+      v = sigmoid_f32(xs);
+    else
+      v = m == -INFINITY ? 0.f : expf(xs - m) / z;
+    if (lane < a.K) {
+      ids[t * a.K + lane] = id;
+      w[t * a.K + lane] = a.scale * v;
+    }
+    __syncwarp();
+  }
 }
 
 // The gradient of the weights: dlogits of one token by one warp, its row built
@@ -302,15 +496,32 @@ static bool valid_router(int dtype, int64_t T, int E, int64_t ld, int K, int sco
 
 static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-template <typename V>
-static int run_router(const void* logits, const float* bias, const RouterArgs& a, int32_t* ids, float* w,
-                      int32_t* dev_status, cudaStream_t stream) {
+template <typename V, int NV>
+static int launch_router(const void* logits, const float* bias, const RouterArgs& a, int32_t* ids, float* w,
+                         int32_t* dev_status, cudaStream_t stream) {
   const size_t smem = (size_t)ROUTER_WARPS * a.E * sizeof(double);
-  if (!raise_smem_limit((const void*)k_router<V>, smem)) return EP_ERR_CUDA;
-  const unsigned grid = (unsigned)((a.T + ROUTER_WARPS - 1) / ROUTER_WARPS);
-  k_router<V><<<grid, ROUTER_WARPS * 32, smem, stream>>>((const V*)logits, bias, a, ids, w, dev_status);
+  if (!raise_smem_limit((const void*)k_router<V, NV>, smem)) return EP_ERR_CUDA;
+  const int64_t want = (a.T + ROUTER_WARPS - 1) / ROUTER_WARPS, most = (int64_t)num_sms() * 8;
+  k_router<V, NV><<<(unsigned)(want < most ? want : most), ROUTER_WARPS * 32, smem, stream>>>((const V*)logits, bias, a,
+                                                                                            ids, w, dev_status);
   count_launch();
   return launch_status();
+}
+
+template <typename V>
+static int run_router(const void* logits, const float* bias, RouterArgs a, int32_t* ids, float* w, int32_t* dev_status,
+                      cudaStream_t stream) {
+  a.lanes_per_group = 32;
+  while (a.lanes_per_group * a.n_group > 32) a.lanes_per_group /= 2;
+  const int len = a.E / a.n_group;
+  a.group_inv = ((1u << 21) + len - 1) / len;
+  // logits a lane: the next of these up from E / 32
+  if (a.E <= 64) return launch_router<V, 2>(logits, bias, a, ids, w, dev_status, stream);
+  if (a.E <= 128) return launch_router<V, 4>(logits, bias, a, ids, w, dev_status, stream);
+  if (a.E <= 256) return launch_router<V, 8>(logits, bias, a, ids, w, dev_status, stream);
+  if (a.E <= 384) return launch_router<V, 12>(logits, bias, a, ids, w, dev_status, stream);
+  if (a.E <= 512) return launch_router<V, 16>(logits, bias, a, ids, w, dev_status, stream);
+  return launch_router<V, 32>(logits, bias, a, ids, w, dev_status, stream);
 }
 
 template <typename V>
@@ -341,7 +552,7 @@ extern "C" int ep_router(const void* logits, int dtype, int64_t T, int E, int64_
       !aligned_to(topk_ids, 4) || !aligned_to(w, 4))
     return EP_ERR_ARG;
   const RouterArgs a{T, ld, E, K, topk_group == n_group ? 1 : n_group, topk_group, group_top,
-                     score == EP_SCORE_SIGMOID, renorm != 0, scale};
+                     score == EP_SCORE_SIGMOID, renorm != 0, scale, 32, 0};
   if (dtype == EP_DTYPE_F32) return run_router<float>(logits, bias, a, topk_ids, w, dev_status, stream);
   if (dtype == EP_DTYPE_BF16) return run_router<__nv_bfloat16>(logits, bias, a, topk_ids, w, dev_status, stream);
   return run_router<__half>(logits, bias, a, topk_ids, w, dev_status, stream);
@@ -356,7 +567,7 @@ extern "C" int ep_router_backward(const float* dw, const void* logits, int dtype
   if (!dw || !logits || !topk_ids || !dlogits || !aligned_to(logits, size) || !aligned_to(dlogits, size) ||
       !aligned_to(dw, 4) || !aligned_to(topk_ids, 4))
     return EP_ERR_ARG;
-  const RouterArgs a{T, ld, E, K, 1, 1, 1, score == EP_SCORE_SIGMOID, renorm != 0, scale};
+  const RouterArgs a{T, ld, E, K, 1, 1, 1, score == EP_SCORE_SIGMOID, renorm != 0, scale, 32, 0};
   if (dtype == EP_DTYPE_F32)
     return run_router_backward<float>(dw, logits, topk_ids, a, ld_out, dlogits, dev_status, stream);
   if (dtype == EP_DTYPE_BF16)
