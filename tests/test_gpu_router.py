@@ -148,7 +148,7 @@ def test_experts_closer_than_32_bit_scores_tell_apart(score, groups, bias):
 
 @gpu
 @pytest.mark.parametrize("E,K", [(64, 8), (96, 32), (1024, 5)])
-@pytest.mark.parametrize("what", ["equal", "lowest", "two values"])
+@pytest.mark.parametrize("what", ["equal", "lowest", "two values", "signed zeros"])
 def test_ties_go_to_the_lower_index(E, K, what):
     import torch
     x = torch.zeros((5, E))
@@ -156,6 +156,8 @@ def test_ties_go_to_the_lower_index(E, K, what):
         x += torch.finfo(torch.float32).min
     if what == "two values":
         x[:, 1::2] = 1.0
+    if what == "signed zeros":
+        x[:, ::3] = -0.0
     ids, w, st = call(x.cuda(), K, score="softmax")
     want = np.arange(K) if what != "two values" else np.concatenate([np.arange(1, E, 2), np.arange(0, E, 2)])[:K]
     assert st == 0

@@ -61,21 +61,49 @@ __device__ __forceinline__ V warp_sum(V v) {
   return v;
 }
 
+__device__ __forceinline__ float warp_fmax(float v) {  // NaN on a lane counts as nothing
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ float ex2_approx(float v) {  // 2^v, off by at most 2^-22 of it
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float v) {  // 1 / v, off by at most 2^-23 of it
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
+
+// e^v for v <= 0 to a few units in the last place: what the product with log2 e
+// loses (found by the fused product) comes back as a factor.
+__device__ __forceinline__ float exp_near(float v) {
+  const float p = v * LOG2E, lost = fmaf(v, LOG2E, -p);
+  return v < -87.f ? expf(v) : fmaf(ex2_approx(p) * LN2, lost, ex2_approx(p));
+}
+
 // s / sum_j s_j of the chosen logits (lane k < K holds x_k, the others -inf),
 // 0 in a row whose chosen logits are all -inf.  Both scores are e^x / (1 + e^x)
 // or e^x over a common factor, so the ratio is taken of numbers scaled by the
 // largest: no sum under- or overflows.
 __device__ __forceinline__ float chosen_ratio(float x, bool sigmoid) {
-  const float m = warp_max(x);
+  const float m = warp_fmax(x);
   if (m == -INFINITY) return 0.f;
   float t;
-  if (!sigmoid)
-    t = expf(x - m);
-  else if (x >= 0.f)
-    t = 1.f / (1.f + expf(-x));
-  else
-    t = expf(x - fminf(m, 0.f)) / (1.f + expf(x));
-  return t / warp_sum(t);
+  if (!sigmoid) {
+    t = exp_near(x - m);
+  } else {
+    const float a = exp_near(-fabsf(x));  // s = 1 / (1 + a) or a / (1 + a)
+    t = x >= 0.f ? 1.f : m >= 0.f ? a : exp_near(x - m);
+    t = __fdividef(t, 1.f + a);
+  }
+  return __fdividef(t, warp_sum(t));
 }
 
 __device__ __forceinline__ float sigmoid_f32(float x) {
@@ -184,12 +212,6 @@ __device__ int select_exact(const RouterArgs& a, const V* __restrict__ row, cons
   return mine;
 }
 
-__device__ __forceinline__ float warp_fmax(float v) {  // NaN on a lane counts as nothing
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
-
 // Bounds of what the fast path's keys are off, from its steps: e^-x by ex2 of a
 // rounded product (|x| 2^-24 and 2^-22 of itself), a sum, a quotient (2^-22), the
 // bias added (2^-24 of the key).  Sigmoid: s (1 - s) |x| <= 0.23, so below 5e-7 of
@@ -199,22 +221,26 @@ __device__ __forceinline__ float key_error(bool sigmoid, float s, float key) {
   return (sigmoid ? 5e-7f : 1e-7f + 4e-6f * s) + 1.2e-7f * fabsf(key);
 }
 
-struct Candidate {
-  float key;
-  int e;
-};
-
 constexpr int HOISTED = 16;  // logits a lane up to which its biases stay in registers
+
+// A candidate as one number, greater where it goes before: the key's bits in the
+// order of their values, then the complement of the expert.
+__device__ __forceinline__ uint64_t pack_candidate(float key, int e) {
+  const uint32_t b = __float_as_uint(key + 0.f);  // -0 ties with 0
+  const uint32_t up = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return (uint64_t)up << 32 | (uint32_t)~e;
+}
+__device__ __forceinline__ int candidate_expert(uint64_t c) { return (int)~(uint32_t)c; }
+__device__ __forceinline__ float candidate_key(uint64_t c) {
+  const uint32_t up = (uint32_t)(c >> 32);
+  return __uint_as_float(up & 0x80000000u ? up ^ 0x80000000u : ~up);
+}
 
 // Lists of a warp: up to 64 candidates, then the first K + 1 in order.
 struct RouterList {
-  Candidate c[64];
-  Candidate sorted[33];
+  uint64_t c[64];
+  uint64_t sorted[34];
 };
-
-__device__ __forceinline__ bool goes_before(const Candidate& a, const Candidate& b) {
-  return a.key > b.key || (a.key == b.key && a.e < b.e);
-}
 
 // The groups to take from, as a mask over groups, from the values at row[0, E) in
 // shared memory; false when two groups at the border are too close to tell.
@@ -258,63 +284,70 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* ro
   return !__any_sync(0xffffffffu, tight);
 }
 
-// One token by one warp in fp32, NV logits a lane.  Lane k < K returns the k-th
-// expert, or every lane -1 where fp32 cannot tell: the caller then takes
-// select_exact.  The K + 1 largest are among the elements that reach the
-// (K + 1)-th largest of the lanes' own maxima: usually few more than K + 1, which
-// are ranked against each other.
-template <typename V, int NV>
+// One token by one warp in fp32, NV logits a lane (all of them there if FULL).
+// Lane k < K returns the k-th expert, or every lane -1 where fp32 cannot tell: the
+// caller then takes select_exact.  The K + 1 largest are among the elements that
+// reach the (K + 1)-th largest of the lanes' own maxima: usually few more than
+// K + 1, which are ranked against each other.  masked: there is a -inf in the row.
+template <typename V, int NV, bool FULL>
 __device__ __forceinline__ int select_fast(const RouterArgs& a, const V* __restrict__ logits, const float (&x)[NV],
-                                           const float (&b)[NV], const float* __restrict__ bias, RouterList* list,
-                                           float* row, float* top_logit, float* total) {
+                                           const float (&b)[NV], const float* __restrict__ bias, bool masked,
+                                           RouterList* list, float* row, float* top_logit, float* total) {
   const int lane = threadIdx.x & 31;
   const bool group_scores = a.n_group > 1 && !bias && a.group_top == 2;
   const bool scores = bias != nullptr || group_scores;
   float key[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) key[j] = x[j];
   float m = -INFINITY, z = 0.f;
-  if (!a.sigmoid && (scores || !a.renorm)) {  // softmax over the row
+  if (!a.sigmoid && (scores || !a.renorm)) {  // softmax over the row; what is not there is -inf
 #pragma unroll
     for (int j = 0; j < NV; ++j) m = fmaxf(m, x[j]);
     m = warp_fmax(m);
+    const float m0 = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      key[j] = m == -INFINITY ? 0.f : __expf(x[j] - m);
-      z += lane + 32 * j < a.E ? key[j] : 0.f;
+      const float p = ex2_approx((x[j] - m0) * LOG2E);
+      sum += p;
+      if (scores) key[j] = p;
     }
-    z = warp_sum(z);
+    z = warp_sum(sum);
   }
   *top_logit = m;
   *total = z;
   if (scores) {
-    const float iz = z > 0.f ? __fdividef(1.f, z) : 0.f;
+    const float iz = z > 0.f ? rcp_approx(z) : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      key[j] = a.sigmoid ? __fdividef(1.f, 1.f + __expf(-x[j])) : key[j] * iz;
-      if (bias) key[j] += NV <= HOISTED ? b[j] : lane + 32 * j < a.E ? bias[lane + 32 * j] : 0.f;
-      if (x[j] == -INFINITY) key[j] = -INFINITY;
+      key[j] = a.sigmoid ? rcp_approx(1.f + ex2_approx(x[j] * -LOG2E)) : key[j] * iz;
+      if (bias) key[j] += NV <= HOISTED ? b[j] : FULL || lane + 32 * j < a.E ? bias[lane + 32 * j] : 0.f;
     }
-  } else {
+    if (masked) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) key[j] = x[j];
-  }
-  uint32_t keep = 0xffffffffu;
-  if (a.n_group > 1) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (lane + 32 * j < a.E) row[lane + 32 * j] = key[j];
-    __syncwarp();
-    if (!keep_groups(a, row, scores, &keep)) return -1;
-    if (group_scores) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) key[j] = x[j];
+      for (int j = 0; j < NV; ++j)
+        if (x[j] == -INFINITY) key[j] = -INFINITY;
     }
   }
   // NaN: not there (past E, or of a group left out)
+  if (a.n_group > 1) {
+    uint32_t keep;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e = lane + 32 * j;
-    const uint32_t g = (uint32_t)e * a.group_inv >> 21;
-    if (e >= a.E || (a.n_group > 1 && !(keep >> g & 1))) key[j] = NAN;
+    for (int j = 0; j < NV; ++j)
+      if (FULL || lane + 32 * j < a.E) row[lane + 32 * j] = key[j];
+    __syncwarp();
+    if (!keep_groups(a, row, scores, &keep)) return -1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (group_scores) key[j] = x[j];
+      const uint32_t g = (uint32_t)(lane + 32 * j) * a.group_inv >> 21;
+      if (!(keep >> g & 1)) key[j] = NAN;
+    }
+  }
+  if (!FULL) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (lane + 32 * j >= a.E) key[j] = NAN;
   }
   float own = NAN;
 #pragma unroll
@@ -325,12 +358,13 @@ __device__ __forceinline__ int select_fast(const RouterArgs& a, const V* __restr
     if (own == t) own = NAN;
   }
   if (isnan(t)) t = -INFINITY;
-  int mine = 0;
+  uint32_t mine = 0;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) mine += key[j] >= t;
+  for (int j = 0; j < NV; ++j) mine |= key[j] >= t ? 1u << j : 0u;
+  const int count = __popc(mine);
   int n = 0, at = 0;
   for (int i = 1;; ++i) {
-    const uint32_t have = __ballot_sync(0xffffffffu, mine >= i);
+    const uint32_t have = __ballot_sync(0xffffffffu, count >= i);
     if (!have) break;
     at += __popc(have & lanemask_lt());
     n += __popc(have);
@@ -339,63 +373,77 @@ __device__ __forceinline__ int select_fast(const RouterArgs& a, const V* __restr
   // at: the lower lanes' candidates (those that have an i-th, summed over i), and so this lane's first place
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (key[j] >= t) list->c[at++] = Candidate{key[j], lane + 32 * j};
+    if (mine >> j & 1) list->c[at++] = pack_candidate(key[j], lane + 32 * j);
+  if (lane == 0 && n < 64) list->c[n] = 0;  // the ranking goes by twos
   __syncwarp();
-  const Candidate none{NAN, INT_MAX};
-  const Candidate c0 = lane < n ? list->c[lane] : none, c1 = lane + 32 < n ? list->c[lane + 32] : none;
-  int r0 = 0, r1 = 0;
-  for (int i = 0; i < n; ++i) {
-    const Candidate o = list->c[i];
-    r0 += goes_before(o, c0);
-    if (n > 32) r1 += goes_before(o, c1);
+  const uint64_t c0 = lane < n ? list->c[lane] : 0;
+  int r0 = 0;
+  for (int i = 0; i < n; i += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list->c + i);
+    r0 += o.x > c0;
+    r0 += o.y > c0;
   }
   if (lane < n && r0 <= a.K) list->sorted[r0] = c0;
-  if (lane + 32 < n && r1 <= a.K) list->sorted[r1] = c1;
+  if (n > 32) {
+    const uint64_t c1 = lane + 32 < n ? list->c[lane + 32] : 0;
+    int r1 = 0;
+    for (int i = 0; i < n; ++i) r1 += list->c[i] > c1;
+    if (lane + 32 < n && r1 <= a.K) list->sorted[r1] = c1;
+  }
   __syncwarp();
   const int have = min(n, a.K + 1);
-  const Candidate c = lane < have ? list->sorted[lane] : none;
-  bool tight = false;
+  const uint64_t c = lane < have ? list->sorted[lane] : 0;
+  const int e = candidate_expert(c);
   if (bias) {
-    const Candidate o = lane + 1 < have ? list->sorted[lane + 1] : none;
-    if (lane < a.K && o.e != INT_MAX && o.key != -INFINITY) {
-      const float bc = bias[c.e], bo = bias[o.e];
-      tight = c.key - o.key <= key_error(a.sigmoid, c.key - bc, c.key) + key_error(a.sigmoid, o.key - bo, o.key);
-      if (tight && bc == bo) tight = to_f32(logits[c.e]) != to_f32(logits[o.e]);  // equal in truth: in order as it is
+    // Neighbours whose difference is within what both are off.  A score of 1 bounds every error; only rows with a
+    // pair that is close by that look at the scores themselves.
+    const float key0 = candidate_key(c), key1 = __shfl_down_sync(0xffffffffu, key0, 1);
+    const int e1 = __shfl_down_sync(0xffffffffu, e, 1);
+    bool tight = lane < a.K && lane + 1 < have && key1 != -INFINITY &&
+                 key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1);
+    if (__any_sync(0xffffffffu, tight)) {
+      if (tight) {
+        const float b0 = bias[e], b1 = bias[e1];
+        tight = key0 - key1 <= key_error(a.sigmoid, key0 - b0, key0) + key_error(a.sigmoid, key1 - b1, key1);
+        if (tight && b0 == b1) tight = to_f32(logits[e]) != to_f32(logits[e1]);  // equal in truth: in order as it is
+      }
+      if (__any_sync(0xffffffffu, tight)) return -1;
     }
   }
   __syncwarp();
-  return __any_sync(0xffffffffu, tight) ? -1 : c.e;
+  return e;
 }
 
-template <typename V, int NV>
+template <typename V, int NV, bool FULL>
 __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3 : 2)
     k_router(const V* __restrict__ logits, const float* __restrict__ bias, RouterArgs a, int32_t* __restrict__ ids,
              float* __restrict__ w, int32_t* dev_status) {
   extern __shared__ double s_key[];  // [warps][E], of select_exact (select_fast uses it as fp32)
-  __shared__ RouterList s_list[ROUTER_WARPS];
+  __shared__ __align__(16) RouterList s_list[ROUTER_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double* mine = s_key + (size_t)warp * a.E;
   float b[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) b[j] = NV <= HOISTED && bias && lane + 32 * j < a.E ? bias[lane + 32 * j] : 0.f;
+  for (int j = 0; j < NV; ++j)
+    b[j] = NV <= HOISTED && bias && (FULL || lane + 32 * j < a.E) ? bias[lane + 32 * j] : 0.f;
   for (int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + warp; t < a.T; t += (int64_t)gridDim.x * ROUTER_WARPS) {
     const V* row = logits + t * a.ld;
     float x[NV];
-    bool bad = false;
+    bool special = false;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) x[j] = lane + 32 * j < a.E ? to_f32(row[lane + 32 * j]) : -INFINITY;
+    for (int j = 0; j < NV; ++j) x[j] = FULL || lane + 32 * j < a.E ? to_f32(row[lane + 32 * j]) : -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) bad |= !(x[j] <= FLT_MAX);
-    bad = __any_sync(0xffffffffu, bad);
-    if (bad) {
-      bool ignore = false;
+    for (int j = 0; j < NV; ++j) special |= !(fabsf(x[j]) <= FLT_MAX) && (FULL || lane + 32 * j < a.E);
+    special = __any_sync(0xffffffffu, special);
+    if (special) {
+      bool bad = false;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) x[j] = clean_logit(x[j], ignore);
-      if (lane == 0) flag(dev_status, EP_DEV_BAD_LOGIT);
+      for (int j = 0; j < NV; ++j) x[j] = clean_logit(x[j], bad);
+      if (__any_sync(0xffffffffu, bad) && lane == 0) flag(dev_status, EP_DEV_BAD_LOGIT);
     }
     float m, z;
-    int id = select_fast<V, NV>(a, row, x, b, bias, s_list + warp, reinterpret_cast<float*>(mine), &m, &z);
-    if (__any_sync(0xffffffffu, id < 0)) id = select_exact(a, row, bias, mine);
+    int id = select_fast<V, NV, FULL>(a, row, x, b, bias, special, s_list + warp, reinterpret_cast<float*>(mine), &m, &z);
+    if (__any_sync(0xffffffffu, lane < a.K && id < 0)) id = select_exact(a, row, bias, mine);
     bool ignore = false;
     const float xs = lane < a.K ? clean_logit(to_f32(row[id]), ignore) : -INFINITY;
     float v;
@@ -404,10 +452,11 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3
     else if (a.sigmoid)
       v = sigmoid_f32(xs);
     else
-      v = m == -INFINITY ? 0.f : expf(xs - m) / z;
+      v = m == -INFINITY ? 0.f : exp_near(xs - m) / z;
     if (lane < a.K) {
-      ids[t * a.K + lane] = id;
-      w[t * a.K + lane] = a.scale * v;
+      const int64_t at = t * a.K + lane;
+      ids[at] = id;
+      w[at] = a.scale * v;
     }
     __syncwarp();
   }
@@ -496,13 +545,13 @@ static bool valid_router(int dtype, int64_t T, int E, int64_t ld, int K, int sco
 
 static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-template <typename V, int NV>
+template <typename V, int NV, bool FULL>
 static int launch_router(const void* logits, const float* bias, const RouterArgs& a, int32_t* ids, float* w,
                          int32_t* dev_status, cudaStream_t stream) {
   const size_t smem = (size_t)ROUTER_WARPS * a.E * sizeof(double);
-  if (!raise_smem_limit((const void*)k_router<V, NV>, smem)) return EP_ERR_CUDA;
+  if (!raise_smem_limit((const void*)k_router<V, NV, FULL>, smem)) return EP_ERR_CUDA;
   const int64_t want = (a.T + ROUTER_WARPS - 1) / ROUTER_WARPS, most = (int64_t)num_sms() * 8;
-  k_router<V, NV><<<(unsigned)(want < most ? want : most), ROUTER_WARPS * 32, smem, stream>>>((const V*)logits, bias, a,
+  k_router<V, NV, FULL><<<(unsigned)(want < most ? want : most), ROUTER_WARPS * 32, smem, stream>>>((const V*)logits, bias, a,
                                                                                             ids, w, dev_status);
   count_launch();
   return launch_status();
@@ -516,12 +565,17 @@ static int run_router(const void* logits, const float* bias, RouterArgs a, int32
   const int len = a.E / a.n_group;
   a.group_inv = ((1u << 21) + len - 1) / len;
   // logits a lane: the next of these up from E / 32
-  if (a.E <= 64) return launch_router<V, 2>(logits, bias, a, ids, w, dev_status, stream);
-  if (a.E <= 128) return launch_router<V, 4>(logits, bias, a, ids, w, dev_status, stream);
-  if (a.E <= 256) return launch_router<V, 8>(logits, bias, a, ids, w, dev_status, stream);
-  if (a.E <= 384) return launch_router<V, 12>(logits, bias, a, ids, w, dev_status, stream);
-  if (a.E <= 512) return launch_router<V, 16>(logits, bias, a, ids, w, dev_status, stream);
-  return launch_router<V, 32>(logits, bias, a, ids, w, dev_status, stream);
+#define EP_ROUTER(nv)                                                                       \
+  if (a.E == 32 * nv) return launch_router<V, nv, true>(logits, bias, a, ids, w, dev_status, stream); \
+  if (a.E < 32 * nv) return launch_router<V, nv, false>(logits, bias, a, ids, w, dev_status, stream)
+  EP_ROUTER(2);
+  EP_ROUTER(4);
+  EP_ROUTER(8);
+  EP_ROUTER(12);
+  EP_ROUTER(16);
+  EP_ROUTER(32);
+#undef EP_ROUTER
+  return EP_ERR_ARG;
 }
 
 template <typename V>
