@@ -123,6 +123,42 @@ def test_router_matches_the_definition(case, masked, dtype):
     assert np.all(np.abs(w - want) <= w_bound(x64, want, ids, scale))
 
 
+MANY = [  # more tokens than there are warps at work: several to a warp
+    (5003, 64, 6, "softmax", None, 1, 1, 1, False, 1.0),
+    (5003, 40, 8, "sigmoid", 0.1, 1, 1, 1, True, 2.5),
+    (4801, 96, 12, "sigmoid", 0.1, 4, 2, 2, True, 1.0),
+    (4801, 33, 20, "softmax", 0.05, 1, 1, 1, True, 1.0),
+    (4801, 32, 32, "sigmoid", None, 1, 1, 1, True, 1.0),
+    (4801, 16, 16, "softmax", 0.1, 1, 1, 1, True, 1.0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "_".join(str(v) for v in c))
+def test_many_tokens(case, masked, dtype):
+    test_router_matches_the_definition(case, masked, dtype)
+
+
+@gpu
+def test_close_keys_among_many_tokens():
+    """Tokens that fp32 cannot decide, next to others of the same warp that it can."""
+    import torch
+    T, E, K = 5001, 32, 4
+    x = logits_of(T, E, torch.float32, 12)
+    x[::3, 5] = x[::3, 9]
+    close = np.nextafter(x[1::7, 3].numpy(), np.float32(np.inf))
+    x[1::7, 4] = torch.from_numpy(close)
+    x[::5, :6] += 3.0
+    bias = np.zeros(E, np.float32)
+    ids, w, st = call(x.cuda(), K, score="sigmoid", bias=bias)
+    want_ids, want = ref_router(x.double().numpy(), K, "sigmoid", bias=bias.astype(np.float64))
+    assert st == 0
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(x.double().numpy(), want, ids, 1.0))
+
+
 @gpu
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])

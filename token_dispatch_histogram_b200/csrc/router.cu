@@ -88,13 +88,15 @@ __device__ __forceinline__ float exp_near(float v) {
   return v < -87.f ? expf(v) : fmaf(ex2_approx(p) * LN2, lost, ex2_approx(p));
 }
 
-// s / sum_j s_j of the chosen logits (lane k < K holds x_k, the others -inf),
-// 0 in a row whose chosen logits are all -inf.  Both scores are e^x / (1 + e^x)
+// s / sum_j s_j of a token's chosen logits, `width` lanes to a token (lane k < K
+// holds x_k, the others -inf); 0 where all of them are -inf.  Both scores are e^x / (1 + e^x)
 // or e^x over a common factor, so the ratio is taken of numbers scaled by the
 // largest: no sum under- or overflows.
-__device__ __forceinline__ float chosen_ratio(float x, bool sigmoid) {
-  const float m = warp_fmax(x);
-  if (m == -INFINITY) return 0.f;
+__device__ __forceinline__ float chosen_ratio(float x, bool sigmoid, int width) {
+  float m = x;
+  for (int d = width >> 1; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const bool none = m == -INFINITY;
+  if (none) m = 0.f;
   float t;
   if (!sigmoid) {
     t = exp_near(x - m);
@@ -103,7 +105,9 @@ __device__ __forceinline__ float chosen_ratio(float x, bool sigmoid) {
     t = x >= 0.f ? 1.f : m >= 0.f ? a : exp_near(x - m);
     t = __fdividef(t, 1.f + a);
   }
-  return __fdividef(t, warp_sum(t));
+  float sum = t;
+  for (int d = width >> 1; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return none ? 0.f : __fdividef(t, sum);
 }
 
 __device__ __forceinline__ float sigmoid_f32(float x) {
@@ -117,6 +121,8 @@ struct RouterArgs {
   int E, K, n_group, topk_group, group_top;
   bool sigmoid, renorm;
   float scale;
+  int width;            // lanes to a token once its experts are chosen
+  bool more;            // there are more than K experts to choose from
   int lanes_per_group;  // 32 / n_group, n_group rounded up to a power of two
   uint32_t group_inv;   // e * group_inv >> 21 == e / (E / n_group) for e < 1024
 };
@@ -223,23 +229,13 @@ __device__ __forceinline__ float key_error(bool sigmoid, float s, float key) {
 
 constexpr int HOISTED = 16;  // logits a lane up to which its biases stay in registers
 
-// A candidate as one number, greater where it goes before: the key's bits in the
-// order of their values, then the complement of the expert.
-__device__ __forceinline__ uint64_t pack_candidate(float key, int e) {
-  const uint32_t b = __float_as_uint(key + 0.f);  // -0 ties with 0
-  const uint32_t up = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-  return (uint64_t)up << 32 | (uint32_t)~e;
-}
-__device__ __forceinline__ int candidate_expert(uint64_t c) { return (int)~(uint32_t)c; }
-__device__ __forceinline__ float candidate_key(uint64_t c) {
-  const uint32_t up = (uint32_t)(c >> 32);
-  return __uint_as_float(up & 0x80000000u ? up ^ 0x80000000u : ~up);
-}
-
-// Lists of a warp: up to 64 candidates, then the first K + 1 in order.
+// Lists of a warp: up to 64 candidates of the token at hand, in any order, and
+// the first K + 1 of each token of a batch, in order.
 struct RouterList {
-  uint64_t c[64];
-  uint64_t sorted[34];
+  float key[68];
+  int e[64];
+  float sorted_key[36];
+  int sorted_e[36];
 };
 
 // The groups to take from, as a mask over groups, from the values at row[0, E) in
@@ -284,15 +280,16 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* ro
   return !__any_sync(0xffffffffu, tight);
 }
 
-// One token by one warp in fp32, NV logits a lane (all of them there if FULL).
-// Lane k < K returns the k-th expert, or every lane -1 where fp32 cannot tell: the
-// caller then takes select_exact.  The K + 1 largest are among the elements that
-// reach the (K + 1)-th largest of the lanes' own maxima: usually few more than
-// K + 1, which are ranked against each other.  masked: there is a -inf in the row.
+// One token by one warp in fp32, NV logits a lane (all of them there if FULL): the
+// K + 1 first experts in order to sorted_key and sorted_e.  False where that cannot
+// be told from here (two groups too close, too many candidates): the caller then
+// takes select_exact.  The K + 1 largest are among the elements that reach the
+// (K + 1)-th largest of the lanes' own maxima: usually few more than K + 1, which
+// are ranked against each other.  masked: there is a -inf in the row.
 template <typename V, int NV, bool FULL>
-__device__ __forceinline__ int select_fast(const RouterArgs& a, const V* __restrict__ logits, const float (&x)[NV],
-                                           const float (&b)[NV], const float* __restrict__ bias, bool masked,
-                                           RouterList* list, float* row, float* top_logit, float* total) {
+__device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x)[NV], const float (&b)[NV],
+                                            const float* __restrict__ bias, bool masked, RouterList* list, float* row,
+                                            float* sorted_key, int* sorted_e, float* top_logit, float* total) {
   const int lane = threadIdx.x & 31;
   const bool group_scores = a.n_group > 1 && !bias && a.group_top == 2;
   const bool scores = bias != nullptr || group_scores;
@@ -330,18 +327,23 @@ __device__ __forceinline__ int select_fast(const RouterArgs& a, const V* __restr
     }
   }
   // NaN: not there (past E, or of a group left out)
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (FULL || lane + 32 * j < a.E) row[lane + 32 * j] = key[j];
   if (a.n_group > 1) {
     uint32_t keep;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (FULL || lane + 32 * j < a.E) row[lane + 32 * j] = key[j];
     __syncwarp();
-    if (!keep_groups(a, row, scores, &keep)) return -1;
+    if (!keep_groups(a, row, scores, &keep)) return false;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (group_scores) key[j] = x[j];
+      if (group_scores) key[j] = x[j]; 
       const uint32_t g = (uint32_t)(lane + 32 * j) * a.group_inv >> 21;
       if (!(keep >> g & 1)) key[j] = NAN;
+    }
+    if (group_scores) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (FULL || lane + 32 * j < a.E) row[lane + 32 * j] = key[j];
     }
   }
   if (!FULL) {
@@ -353,9 +355,12 @@ __device__ __forceinline__ int select_fast(const RouterArgs& a, const V* __restr
 #pragma unroll
   for (int j = 0; j < NV; ++j) own = fmaxf(own, key[j]);
   float t = NAN;
-  for (int k = 0; k <= a.K; ++k) {
-    t = warp_fmax(own);
-    if (own == t) own = NAN;
+  for (int k = 0; k <= a.K; k += 3) {  // up to two more than needed: t is then lower, and all that reach it are taken
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      t = warp_fmax(own);
+      if (own == t) own = NAN;
+    }
   }
   if (isnan(t)) t = -INFINITY;
   uint32_t mine = 0;
@@ -369,51 +374,52 @@ __device__ __forceinline__ int select_fast(const RouterArgs& a, const V* __restr
     at += __popc(have & lanemask_lt());
     n += __popc(have);
   }
-  if (n > 64) return -1;
+  if (n > 64) return false;
   // at: the lower lanes' candidates (those that have an i-th, summed over i), and so this lane's first place
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (mine >> j & 1) list->c[at++] = pack_candidate(key[j], lane + 32 * j);
-  if (lane == 0 && n < 64) list->c[n] = 0;  // the ranking goes by twos
-  __syncwarp();
-  const uint64_t c0 = lane < n ? list->c[lane] : 0;
-  int r0 = 0;
-  for (int i = 0; i < n; i += 2) {
-    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list->c + i);
-    r0 += o.x > c0;
-    r0 += o.y > c0;
+  for (; mine; mine &= mine - 1) {
+    const int e = lane + 32 * (__ffs(mine) - 1);
+    list->key[at] = row[e];
+    list->e[at++] = e;
   }
-  if (lane < n && r0 <= a.K) list->sorted[r0] = c0;
-  if (n > 32) {
-    const uint64_t c1 = lane + 32 < n ? list->c[lane + 32] : 0;
-    int r1 = 0;
-    for (int i = 0; i < n; ++i) r1 += list->c[i] > c1;
-    if (lane + 32 < n && r1 <= a.K) list->sorted[r1] = c1;
-  }
+  if (lane < 4) list->key[n + lane] = NAN;  // the ranking goes by fours
   __syncwarp();
   const int have = min(n, a.K + 1);
-  const uint64_t c = lane < have ? list->sorted[lane] : 0;
-  const int e = candidate_expert(c);
-  if (bias) {
-    // Neighbours whose difference is within what both are off.  A score of 1 bounds every error; only rows with a
-    // pair that is close by that look at the scores themselves.
-    const float key0 = candidate_key(c), key1 = __shfl_down_sync(0xffffffffu, key0, 1);
-    const int e1 = __shfl_down_sync(0xffffffffu, e, 1);
-    bool tight = lane < a.K && lane + 1 < have && key1 != -INFINITY &&
-                 key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1);
-    if (__any_sync(0xffffffffu, tight)) {
-      if (tight) {
-        const float b0 = bias[e], b1 = bias[e1];
-        tight = key0 - key1 <= key_error(a.sigmoid, key0 - b0, key0) + key_error(a.sigmoid, key1 - b1, key1);
-        if (tight && b0 == b1) tight = to_f32(logits[e]) != to_f32(logits[e1]);  // equal in truth: in order as it is
+  if (n <= 32 && have <= 31) {
+    const float k0 = lane < n ? list->key[lane] : NAN;
+    int r0 = 0;
+    for (int i = 0; i < n; i += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(list->key + i);
+      r0 += o.x > k0;
+      r0 += o.y > k0;
+      r0 += o.z > k0;
+      r0 += o.w > k0;
+    }
+    const bool in = lane < n && r0 < have;
+    if (__reduce_or_sync(0xffffffffu, in ? 1u << r0 : 0u) == (1u << have) - 1) {  // no two of them have one rank
+      if (in) {
+        sorted_key[r0] = k0;
+        sorted_e[r0] = list->e[lane];
       }
-      if (__any_sync(0xffffffffu, tight)) return -1;
+      return true;
     }
   }
-  __syncwarp();
-  return e;
+  for (int i = lane; i < n; i += 32) {  // equal keys, or many candidates
+    const float k0 = list->key[i];
+    const int e0 = list->e[i];
+    int r = 0;
+    for (int j = 0; j < n; ++j) r += list->key[j] > k0 || (list->key[j] == k0 && list->e[j] < e0);
+    if (r < have) {
+      sorted_key[r] = k0;
+      sorted_e[r] = e0;
+    }
+  }
+  return true;
 }
 
+// A warp takes 32 / width tokens at a time: one after the other as far as the
+// choice goes, then together, width lanes a token (the next power of two from K,
+// at least 8), for what concerns the K chosen ones only.  A warp to a token the
+// whole way took 420 us where this takes 365 (524,288 tokens, 384 experts).
 template <typename V, int NV, bool FULL>
 __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3 : 2)
     k_router(const V* __restrict__ logits, const float* __restrict__ bias, RouterArgs a, int32_t* __restrict__ ids,
@@ -422,41 +428,87 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3
   __shared__ __align__(16) RouterList s_list[ROUTER_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double* mine = s_key + (size_t)warp * a.E;
+  RouterList* list = s_list + warp;
+  const int width = a.width, batch = 32 / width, of = lane / width, k = lane % width;
   float b[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
     b[j] = NV <= HOISTED && bias && (FULL || lane + 32 * j < a.E) ? bias[lane + 32 * j] : 0.f;
-  for (int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + warp; t < a.T; t += (int64_t)gridDim.x * ROUTER_WARPS) {
-    const V* row = logits + t * a.ld;
-    float x[NV];
-    bool special = false;
+  for (int64_t t0 = ((int64_t)blockIdx.x * ROUTER_WARPS + warp) * batch; t0 < a.T;
+       t0 += (int64_t)gridDim.x * ROUTER_WARPS * batch) {
+    const int n = (int)min((int64_t)batch, a.T - t0);
+    float m = 0.f, z = 0.f;     // softmax of this lane's token
+    uint32_t exact = 0;         // tokens whose choice is from select_exact
+    for (int i = 0; i < n; ++i) {
+      const V* row = logits + (t0 + i) * a.ld;
+      float x[NV];
+      bool special = false;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) x[j] = FULL || lane + 32 * j < a.E ? to_f32(row[lane + 32 * j]) : -INFINITY;
+      for (int j = 0; j < NV; ++j) x[j] = FULL || lane + 32 * j < a.E ? to_f32(row[lane + 32 * j]) : -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) special |= !(fabsf(x[j]) <= FLT_MAX) && (FULL || lane + 32 * j < a.E);
-    special = __any_sync(0xffffffffu, special);
-    if (special) {
-      bool bad = false;
+      for (int j = 0; j < NV; ++j) special |= !(fabsf(x[j]) <= FLT_MAX) && (FULL || lane + 32 * j < a.E);
+      special = __any_sync(0xffffffffu, special);
+      if (special) {
+        bool bad = false;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) x[j] = clean_logit(x[j], bad);
-      if (__any_sync(0xffffffffu, bad) && lane == 0) flag(dev_status, EP_DEV_BAD_LOGIT);
+        for (int j = 0; j < NV; ++j) x[j] = clean_logit(x[j], bad);
+        if (__any_sync(0xffffffffu, bad) && lane == 0) flag(dev_status, EP_DEV_BAD_LOGIT);
+      }
+      float mi, zi;
+      int* to = list->sorted_e + i * (a.K + 1);
+      if (!select_fast<V, NV, FULL>(a, x, b, bias, special, list, reinterpret_cast<float*>(mine),
+                                    list->sorted_key + i * (a.K + 1), to, &mi, &zi)) {
+        __syncwarp();
+        const int id = select_exact(a, row, bias, mine);
+        if (lane < a.K) to[lane] = id;
+        exact |= 1u << i;
+      }
+      if (of == i) {
+        m = mi;
+        z = zi;
+      }
+      __syncwarp();
     }
-    float m, z;
-    int id = select_fast<V, NV, FULL>(a, row, x, b, bias, special, s_list + warp, reinterpret_cast<float*>(mine), &m, &z);
-    if (__any_sync(0xffffffffu, lane < a.K && id < 0)) id = select_exact(a, row, bias, mine);
+    const int at = of * (a.K + 1) + k;
+    const bool live = of < n && k < a.K;
+    const V* row = logits + (t0 + of) * a.ld;
+    int id = live ? list->sorted_e[at] : 0;
+    if (bias) {
+      // Neighbours whose difference is within what both are off.  (The (K + 1)-th is there unless there are only K.)
+      bool tight = false;
+      if (live && !(exact >> of & 1) && (k + 1 < a.K || a.more)) {
+        const float key0 = list->sorted_key[at], key1 = list->sorted_key[at + 1];
+        // a score of 1 bounds every error: only where that is not enough the scores themselves are looked at
+        if (key1 != -INFINITY && key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1)) {
+          const int e1 = list->sorted_e[at + 1];
+          const float b0 = bias[id], b1 = bias[e1];
+          tight = key0 - key1 <= key_error(a.sigmoid, key0 - b0, key0) + key_error(a.sigmoid, key1 - b1, key1);
+          if (tight && b0 == b1) tight = to_f32(row[id]) != to_f32(row[e1]);  // equal in truth: in order as it is
+        }
+      }
+      uint32_t again = __ballot_sync(0xffffffffu, tight);
+      while (again) {
+        const int i = (__ffs(again) - 1) / width;
+        const int e = select_exact(a, logits + (t0 + i) * a.ld, bias, mine);
+        const int back = __shfl_sync(0xffffffffu, e, k);
+        if (of == i && live) id = back;
+        again &= ~((width == 32 ? 0xffffffffu : (1u << width) - 1) << (i * width));
+        __syncwarp();
+      }
+    }
     bool ignore = false;
-    const float xs = lane < a.K ? clean_logit(to_f32(row[id]), ignore) : -INFINITY;
+    const float xs = live ? clean_logit(to_f32(row[id]), ignore) : -INFINITY;
     float v;
     if (a.renorm)
-      v = chosen_ratio(xs, a.sigmoid);
+      v = chosen_ratio(xs, a.sigmoid, width);
     else if (a.sigmoid)
       v = sigmoid_f32(xs);
     else
       v = m == -INFINITY ? 0.f : exp_near(xs - m) / z;
-    if (lane < a.K) {
-      const int64_t at = t * a.K + lane;
-      ids[at] = id;
-      w[at] = a.scale * v;
+    if (live) {
+      const int64_t to = (t0 + of) * a.K + k;
+      ids[to] = id;
+      w[to] = a.scale * v;
     }
     __syncwarp();
   }
@@ -498,7 +550,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32)
   if (a.sigmoid || a.renorm) {
     for (int e = lane; e < a.E; e += 32) out[e] = 0.f;
     if (a.renorm) {
-      const float r = chosen_ratio(x, a.sigmoid);
+      const float r = chosen_ratio(x, a.sigmoid, 32);
       v = r * (d - warp_sum(d * r));
       if (a.sigmoid) v *= sigmoid_f32(-x);
     } else {
@@ -550,7 +602,7 @@ static int launch_router(const void* logits, const float* bias, const RouterArgs
                          int32_t* dev_status, cudaStream_t stream) {
   const size_t smem = (size_t)ROUTER_WARPS * a.E * sizeof(double);
   if (!raise_smem_limit((const void*)k_router<V, NV, FULL>, smem)) return EP_ERR_CUDA;
-  const int64_t want = (a.T + ROUTER_WARPS - 1) / ROUTER_WARPS, most = (int64_t)num_sms() * 8;
+  const int64_t per = ROUTER_WARPS * (32 / a.width), want = (a.T + per - 1) / per, most = (int64_t)num_sms() * 8;
   k_router<V, NV, FULL><<<(unsigned)(want < most ? want : most), ROUTER_WARPS * 32, smem, stream>>>((const V*)logits, bias, a,
                                                                                             ids, w, dev_status);
   count_launch();
@@ -563,6 +615,9 @@ static int run_router(const void* logits, const float* bias, RouterArgs a, int32
   a.lanes_per_group = 32;
   while (a.lanes_per_group * a.n_group > 32) a.lanes_per_group /= 2;
   const int len = a.E / a.n_group;
+  a.more = (a.n_group == 1 ? a.E : a.topk_group * len) > a.K;
+  // few tokens: one to a warp, they are all at work at once
+  a.width = a.T <= (int64_t)num_sms() * 32 ? 32 : a.K <= 8 ? 8 : a.K <= 16 ? 16 : 32;
   a.group_inv = ((1u << 21) + len - 1) / len;
   // logits a lane: the next of these up from E / 32
 #define EP_ROUTER(nv)                                                                       \
@@ -606,7 +661,7 @@ extern "C" int ep_router(const void* logits, int dtype, int64_t T, int E, int64_
       !aligned_to(topk_ids, 4) || !aligned_to(w, 4))
     return EP_ERR_ARG;
   const RouterArgs a{T, ld, E, K, topk_group == n_group ? 1 : n_group, topk_group, group_top,
-                     score == EP_SCORE_SIGMOID, renorm != 0, scale, 32, 0};
+                     score == EP_SCORE_SIGMOID, renorm != 0, scale, 32, true, 32, 0};
   if (dtype == EP_DTYPE_F32) return run_router<float>(logits, bias, a, topk_ids, w, dev_status, stream);
   if (dtype == EP_DTYPE_BF16) return run_router<__nv_bfloat16>(logits, bias, a, topk_ids, w, dev_status, stream);
   return run_router<__half>(logits, bias, a, topk_ids, w, dev_status, stream);
@@ -621,7 +676,7 @@ extern "C" int ep_router_backward(const float* dw, const void* logits, int dtype
   if (!dw || !logits || !topk_ids || !dlogits || !aligned_to(logits, size) || !aligned_to(dlogits, size) ||
       !aligned_to(dw, 4) || !aligned_to(topk_ids, 4))
     return EP_ERR_ARG;
-  const RouterArgs a{T, ld, E, K, 1, 1, 1, score == EP_SCORE_SIGMOID, renorm != 0, scale, 32, 0};
+  const RouterArgs a{T, ld, E, K, 1, 1, 1, score == EP_SCORE_SIGMOID, renorm != 0, scale, 32, true, 32, 0};
   if (dtype == EP_DTYPE_F32)
     return run_router_backward<float>(dw, logits, topk_ids, a, ld_out, dlogits, dev_status, stream);
   if (dtype == EP_DTYPE_BF16)
