@@ -304,7 +304,7 @@ def check_backward(got, want, mag, x):
 @pytest.mark.parametrize("masked", [0.0, 0.3])
 @pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
 @pytest.mark.parametrize("T,E,K", [(1, 1, 1), (1, 256, 8), (65, 64, 6), (33, 17, 17), (9, 1024, 32), (200, 384, 8),
-                                   (21, 100, 5)])
+                                   (21, 100, 5), (5003, 64, 6), (4801, 45, 12), (4801, 300, 20)])
 def test_backward_matches_the_jacobian(T, E, K, score, renorm, masked, dtype):
     import torch
     import token_dispatch_histogram_b200 as tdh
@@ -348,12 +348,14 @@ def test_backward_matches_differences_of_the_forward(score, renorm):
 
 
 @gpu
-def test_backward_of_repeated_and_bad_ids():
+@pytest.mark.parametrize("T", [4, 4904])
+def test_backward_of_repeated_and_bad_ids(T):
     import torch
     import token_dispatch_histogram_b200 as tdh
-    T, E, K = 4, 12, 5
+    E, K = 12, 5
     x = logits_of(T, E, torch.float32, 8)
     ids = np.array([[3, 3, 3, 1, 0], [2, 5, 2, 5, 2], [0, 12, -1, 4, 7], [-1, -1, 99, -5, 1 << 30]], np.int32)
+    ids = np.tile(ids, (T // 4, 1))
     dw = torch.randn((T, K), generator=torch.Generator().manual_seed(1))
     for score in ("softmax", "sigmoid"):
         for renorm in (True, False):

@@ -514,78 +514,165 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3
   }
 }
 
-// The gradient of the weights: dlogits of one token by one warp, its row built
-// in shared memory and written once.  With r_k = s_k / sum_j s_j:
+// Four consecutive elements as fp32, and back.
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 q = *reinterpret_cast<const float4*>(p);
+  v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+}
+template <typename V>
+__device__ __forceinline__ void load4(const V* p, float* v) {
+  const uint2 q = *reinterpret_cast<const uint2*>(p);
+  const V* h = reinterpret_cast<const V*>(&q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = to_f32(h[i]);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <typename V>
+__device__ __forceinline__ void store4(V* p, const float* v) {
+  uint2 q;
+  V* h = reinterpret_cast<V*>(&q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = from_f32<V>(v[i]);
+  *reinterpret_cast<uint2*>(p) = q;
+}
+
+// The gradient of the weights.  With r_k = s_k / sum_j s_j:
 //   softmax, renorm   dx_k = scale r_k (dw_k - i),            i = sum_j dw_j r_j
 //   sigmoid, renorm   dx_k = scale r_k (1 - s_k) (dw_k - i)
 //   sigmoid           dx_k = scale s_k (1 - s_k) dw_k
 //   softmax           dx_e = scale s_e ([e chosen] dw_e - i), i = sum_j dw_j s_j
 // Only the last touches experts that were not chosen (and has to read the row).
 // An expert that stands twice among a token's ids gets the sum of its terms.
-template <typename V>
+//
+// Bound by writing dlogits.  As in the router, a warp takes 32 / width tokens: the
+// chosen logits of all of them at once, then row by row.  The chosen experts'
+// terms are laid into a row of zeros in shared memory, the row goes out in vectors
+// of four (VEC: the rows are aligned to that), and only the places that were
+// written are zeroed again.
+template <typename V, int NC, bool VEC>
 __global__ void __launch_bounds__(ROUTER_WARPS * 32)
     k_router_backward(const float* __restrict__ dw, const V* __restrict__ logits, const int32_t* __restrict__ ids,
                       RouterArgs a, int64_t ld_out, V* __restrict__ dlogits, int32_t* dev_status) {
-  extern __shared__ float s_row[];  // [warps][E]
+  extern __shared__ __align__(16) float s_row[];  // [warps][NC * 128]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * ROUTER_WARPS + warp;
-  if (t >= a.T) return;
-  const V* row = logits + t * a.ld;
-  float* out = s_row + (size_t)warp * a.E;
-  bool bad = false;
-  int id = -1;
-  float x = -INFINITY, d = 0.f;
-  bool bad_id = false;
-  if (lane < a.K) {
-    id = ids[t * a.K + lane];
-    bad_id = id < 0 || id >= a.E;
-    if (!bad_id) {
-      x = clean_logit(to_f32(row[id]), bad);
-      d = dw[t * a.K + lane];
-    } else {
-      id = -1;
+  float* out = s_row + warp * (NC * 128);
+  const int width = a.width, batch = 32 / width, of = lane / width, k = lane % width;
+  const bool dense = !a.sigmoid && !a.renorm;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) *reinterpret_cast<float4*>(out + c * 128 + lane * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncwarp();
+  uint32_t bits = 0;
+  for (int64_t t0 = ((int64_t)blockIdx.x * ROUTER_WARPS + warp) * batch; t0 < a.T;
+       t0 += (int64_t)gridDim.x * ROUTER_WARPS * batch) {
+    const int n = (int)min((int64_t)batch, a.T - t0);
+    bool bad = false;
+    int id = -1;
+    float x = -INFINITY, d = 0.f;
+    if (of < n && k < a.K) {
+      const int64_t at = (t0 + of) * a.K + k;
+      id = ids[at];
+      if (id < 0 || id >= a.E) {
+        bits |= EP_DEV_BAD_EXPERT_ID;
+        id = -1;
+      } else {
+        d = dw[at];
+        x = clean_logit(to_f32(logits[(t0 + of) * a.ld + id]), bad);
+      }
     }
-  }
-  float v;  // this lane's term of dlogits[id]
-  if (a.sigmoid || a.renorm) {
-    for (int e = lane; e < a.E; e += 32) out[e] = 0.f;
+    float v = 0.f;  // this lane's term of dlogits[id], without the scale
     if (a.renorm) {
-      const float r = chosen_ratio(x, a.sigmoid, 32);
-      v = r * (d - warp_sum(d * r));
+      const float r = chosen_ratio(x, a.sigmoid, width);
+      float i = d * r;
+      for (int s = width >> 1; s; s >>= 1) i += __shfl_xor_sync(0xffffffffu, i, s);
+      v = r * (d - i);
       if (a.sigmoid) v *= sigmoid_f32(-x);
-    } else {
+    } else if (a.sigmoid) {
       v = d * sigmoid_f32(x) * sigmoid_f32(-x);
     }
-  } else {
-    float m = -INFINITY, z = 0.f;
-    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, clean_logit(to_f32(row[e]), bad));
-    m = warp_max(m);
-    const float m0 = m == -INFINITY ? 0.f : m;  // a row of -inf has scores of 0
-    for (int e = lane; e < a.E; e += 32) z += expf(clean_logit(to_f32(row[e]), bad) - m0);
-    z = warp_sum(z);
-    const float iz = z > 0.f ? 1.f / z : 0.f;
-    v = d * (expf(x - m0) * iz);
-    const float i = warp_sum(v);
-    for (int e = lane; e < a.E; e += 32) out[e] = -i * a.scale * (expf(clean_logit(to_f32(row[e]), bad) - m0) * iz);
-  }
-  __syncwarp();
-  v *= a.scale;
-  const uint32_t same = __match_any_sync(0xffffffffu, id);
-  if (__any_sync(0xffffffffu, id >= 0 && (same & (same - 1)))) {  // the same expert twice: one lane adds all, in order
-    float sum = 0.f;
-    for (int j = 0; j < a.K; ++j) {
-      const float o = __shfl_sync(0xffffffffu, v, j);
-      if (same >> j & 1) sum += o;
+    // of lanes with the same expert of the same token, the first lays down the sum of all, in order
+    uint32_t same = 0;
+    for (int j = 0; j < a.K; ++j) same |= __shfl_sync(0xffffffffu, id, of * width + j) == id ? 1u << j : 0u;
+    const bool lead = id >= 0 && (same & ((1u << k) - 1)) == 0;
+    const bool twice = __any_sync(0xffffffffu, id >= 0 && (same & (same - 1)));
+    for (int i = 0; i < n; ++i) {
+      const V* row = logits + (t0 + i) * a.ld;
+      V* to = dlogits + (t0 + i) * ld_out;
+      float p[NC][4], inner = 0.f;
+      if (dense) {
+        float m = -INFINITY, z = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[c][j] = -INFINITY;
+          const int e = c * 128 + lane * 4;
+          if (VEC) {
+            if (e < a.E) load4(row + e, p[c]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (e + j < a.E) p[c][j] = to_f32(row[e + j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            p[c][j] = clean_logit(p[c][j], bad);
+            m = fmaxf(m, p[c][j]);
+          }
+        }
+        m = warp_fmax(m);
+        const float m0 = m == -INFINITY ? 0.f : m;  // a row of -inf has scores of 0
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z += p[c][j] = exp_near(p[c][j] - m0);
+        z = warp_sum(z);
+        const float iz = z > 0.f ? 1.f / z : 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[c][j] *= iz;
+        float s = of == i ? d * (exp_near(x - m0) * iz) : 0.f;
+        if (of == i) v = s;
+        inner = warp_sum(s) * a.scale;
+      }
+      float mine = a.scale * v;
+      if (twice) {
+        float sum = 0.f;
+        for (int j = 0; j < a.K; ++j) {
+          const float o = __shfl_sync(0xffffffffu, mine, of * width + j);
+          if (same >> j & 1) sum += o;
+        }
+        mine = sum;
+      }
+      if (lead && of == i) out[id] = mine;
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int e = c * 128 + lane * 4;
+        if (e < a.E) {
+          const float4 q = *reinterpret_cast<const float4*>(out + e);
+          float o[4] = {q.x, q.y, q.z, q.w};
+          if (dense) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] -= inner * p[c][j];
+          }
+          if (VEC) {
+            store4(to + e, o);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (e + j < a.E) to[e + j] = from_f32<V>(o[j]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lead && of == i) out[id] = 0.f;
     }
-    if (id >= 0 && (same & lanemask_lt()) == 0) out[id] += sum;
-  } else if (id >= 0) {
-    out[id] += v;
+    if (bad) bits |= EP_DEV_BAD_LOGIT;
+    __syncwarp();
   }
-  __syncwarp();
-  V* to = dlogits + t * ld_out;
-  for (int e = lane; e < a.E; e += 32) to[e] = from_f32<V>(out[e]);
-  const uint32_t bits = (__any_sync(0xffffffffu, bad) ? EP_DEV_BAD_LOGIT : 0) |
-                        (__any_sync(0xffffffffu, bad_id) ? EP_DEV_BAD_EXPERT_ID : 0);
+  bits = __reduce_or_sync(0xffffffffu, bits);
   if (bits && lane == 0) flag(dev_status, bits);
 }
 
@@ -596,6 +683,11 @@ static bool valid_router(int dtype, int64_t T, int E, int64_t ld, int K, int sco
 }
 
 static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Few tokens: one to a warp, they are all at work at once.
+static int router_width(const RouterArgs& a) {
+  return a.T <= (int64_t)num_sms() * 32 ? 32 : a.K <= 8 ? 8 : a.K <= 16 ? 16 : 32;
+}
 
 template <typename V, int NV, bool FULL>
 static int launch_router(const void* logits, const float* bias, const RouterArgs& a, int32_t* ids, float* w,
@@ -616,8 +708,7 @@ static int run_router(const void* logits, const float* bias, RouterArgs a, int32
   while (a.lanes_per_group * a.n_group > 32) a.lanes_per_group /= 2;
   const int len = a.E / a.n_group;
   a.more = (a.n_group == 1 ? a.E : a.topk_group * len) > a.K;
-  // few tokens: one to a warp, they are all at work at once
-  a.width = a.T <= (int64_t)num_sms() * 32 ? 32 : a.K <= 8 ? 8 : a.K <= 16 ? 16 : 32;
+  a.width = router_width(a);
   a.group_inv = ((1u << 21) + len - 1) / len;
   // logits a lane: the next of these up from E / 32
 #define EP_ROUTER(nv)                                                                       \
@@ -633,16 +724,34 @@ static int run_router(const void* logits, const float* bias, RouterArgs a, int32
   return EP_ERR_ARG;
 }
 
-template <typename V>
-static int run_router_backward(const float* dw, const void* logits, const int32_t* ids, const RouterArgs& a,
-                               int64_t ld_out, void* dlogits, int32_t* dev_status, cudaStream_t stream) {
-  const size_t smem = (size_t)ROUTER_WARPS * a.E * sizeof(float);
-  if (!raise_smem_limit((const void*)k_router_backward<V>, smem)) return EP_ERR_CUDA;
-  const unsigned grid = (unsigned)((a.T + ROUTER_WARPS - 1) / ROUTER_WARPS);
-  k_router_backward<V>
-      <<<grid, ROUTER_WARPS * 32, smem, stream>>>(dw, (const V*)logits, ids, a, ld_out, (V*)dlogits, dev_status);
+template <typename V, int NC, bool VEC>
+static int launch_backward(const float* dw, const void* logits, const int32_t* ids, const RouterArgs& a, int64_t ld_out,
+                           void* dlogits, int32_t* dev_status, cudaStream_t stream) {
+  const size_t smem = (size_t)ROUTER_WARPS * NC * 128 * sizeof(float);
+  if (!raise_smem_limit((const void*)k_router_backward<V, NC, VEC>, smem)) return EP_ERR_CUDA;
+  const int64_t per = ROUTER_WARPS * (32 / a.width), want = (a.T + per - 1) / per, most = (int64_t)num_sms() * 8;
+  k_router_backward<V, NC, VEC><<<(unsigned)(want < most ? want : most), ROUTER_WARPS * 32, smem, stream>>>(
+      dw, (const V*)logits, ids, a, ld_out, (V*)dlogits, dev_status);
   count_launch();
   return launch_status();
+}
+
+template <typename V>
+static int run_router_backward(const float* dw, const void* logits, const int32_t* ids, RouterArgs a, int64_t ld_out,
+                               void* dlogits, int32_t* dev_status, cudaStream_t stream) {
+  a.width = router_width(a);
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && ld_out % 4 == 0 && aligned_to(logits, 4 * sizeof(V)) &&
+                   aligned_to(dlogits, 4 * sizeof(V));
+#define EP_BACKWARD(nc)                                                                                            \
+  if (a.E <= 128 * nc)                                                                                             \
+  return vec ? launch_backward<V, nc, true>(dw, logits, ids, a, ld_out, dlogits, dev_status, stream)               \
+             : launch_backward<V, nc, false>(dw, logits, ids, a, ld_out, dlogits, dev_status, stream)
+  EP_BACKWARD(1);
+  EP_BACKWARD(2);
+  EP_BACKWARD(4);
+  EP_BACKWARD(8);
+#undef EP_BACKWARD
+  return EP_ERR_ARG;
 }
 
 }  // namespace ep
