@@ -8,7 +8,6 @@ If libep.so is missing the import fails.
 
 Device memory and streams come from PyTorch; nothing here computes.
 """
-import contextlib
 import ctypes
 import os
 
@@ -161,35 +160,51 @@ def _dtype(t, *dts):
         raise TypeError(f"dtype {t.dtype}, expected one of {dts}")
 
 
-def _rows(t):
-    """Pointer of a 2-d tensor whose rows are contiguous, at any row stride."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("expected a 2-d tensor with contiguous rows")
+# The calls around the path (router, experts' products, optimizer) are made with
+# few tokens too, where the host's time counts: addresses go as plain integers, and
+# a device or stream object is only made where the caller's differ.
+
+def _at(t):
+    """Address of a contiguous CUDA tensor (None: none)."""
+    if t is None:
+        return None
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
 
 
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _rows(t):
+    """Address and row stride of a 2-d tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a 2-d tensor with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def _shape(what, t, *shape):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
 
 
-@contextlib.contextmanager
-def _device_of(first, *others):
-    """The tensors' device current (they must share one), whatever the caller's
-    current device is."""
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    if not first.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    with torch.cuda.device(first.device):
-        yield
+def _launch(name, args, stream, *tensors):
+    """Call `name` with args and a stream (the current one of the tensors' device
+    unless given) while the tensors' device is current; they must share one."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"tensors on {dev} and a stream on {stream.device}")
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    f = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        _check(name, f(*args, raw))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, f(*args, raw))
 
 
 def version():
@@ -567,12 +582,12 @@ def _router_args(logits, topk_ids, w, score):
     _dtype(w, torch.float32)
     if score not in _SCORES:
         raise ValueError(f"score {score!r}, expected one of {sorted(_SCORES)}")
-    _rows(logits)
+    x, ld = _rows(logits)
     T, E = logits.shape
     K = topk_ids.shape[1]
     _shape("topk_ids", topk_ids, T, K)
     _shape("gate weights", w, T, K)
-    return T, E, K, _LOGIT_DTYPES[logits.dtype], _SCORES[score]
+    return x, T, E, ld, K, _LOGIT_DTYPES[logits.dtype], _SCORES[score]
 
 
 def ep_router(logits, topk_ids, w, score="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renorm=True,
@@ -581,28 +596,24 @@ def ep_router(logits, topk_ids, w, score="softmax", bias=None, n_group=1, topk_g
     [T, E] (fp32, bf16 or fp16, any row stride); K = topk_ids.shape[1].  score:
     "softmax" or "sigmoid"; bias [E] moves the choice only; of the n_group
     groups only the topk_group best are taken from (see ep.h)."""
-    T, E, K, dt, sc = _router_args(logits, topk_ids, w, score)
+    x, T, E, ld, K, dt, sc = _router_args(logits, topk_ids, w, score)
     if bias is not None:
         _dtype(bias, torch.float32)
         _shape("bias", bias, E)
-    with _device_of(logits, topk_ids, w, bias, dev_status):
-        _check("ep_router", lib().ep_router(_rows(logits), dt, T, E, _ld(logits), K, sc, _p(bias), n_group,
-                                            topk_group, group_top, int(bool(renorm)), scale, _p(topk_ids), _p(w),
-                                            _p(dev_status), _s(stream)))
+    _launch("ep_router", (x, dt, T, E, ld, K, sc, _at(bias), n_group, topk_group, group_top, bool(renorm), scale,
+                          _at(topk_ids), _at(w), _at(dev_status)), stream, logits, topk_ids, w, bias, dev_status)
 
 
 def ep_router_backward(dw, logits, topk_ids, dlogits, score="softmax", renorm=True, scale=1.0, dev_status=None,
                        stream=None):
     """dlogits [T, E] from the gradient dw [T, K] of the gate weights; score,
     renorm and scale as ep_router had them."""
-    T, E, K, dt, sc = _router_args(logits, topk_ids, dw, score)
+    x, T, E, ld, K, dt, sc = _router_args(logits, topk_ids, dw, score)
     _dtype(dlogits, logits.dtype)
     _shape("dlogits", dlogits, T, E)
-    with _device_of(logits, dw, topk_ids, dlogits, dev_status):
-        _check("ep_router_backward",
-               lib().ep_router_backward(_p(dw), _rows(logits), dt, T, E, _ld(logits), _p(topk_ids), K, sc,
-                                        int(bool(renorm)), scale, _rows(dlogits), _ld(dlogits), _p(dev_status),
-                                        _s(stream)))
+    dx, ld_out = _rows(dlogits)
+    _launch("ep_router_backward", (_at(dw), x, dt, T, E, ld, _at(topk_ids), K, sc, bool(renorm), scale, dx, ld_out,
+                                   _at(dev_status)), stream, logits, dw, topk_ids, dlogits, dev_status)
 
 
 def _slots(cu_seqlens, slot_order, rep_expert):
@@ -613,7 +624,7 @@ def _slots(cu_seqlens, slot_order, rep_expert):
     n = max(0, cu_seqlens.numel() - 1)
     if slot_order is not None:
         _shape("slot_order", slot_order, n)
-    return _p(cu_seqlens), n, _p(slot_order), _p(rep_expert), 0 if rep_expert is None else rep_expert.numel()
+    return _at(cu_seqlens), n, _at(slot_order), _at(rep_expert), 0 if rep_expert is None else rep_expert.numel()
 
 
 def _bf16(*ts):
@@ -631,10 +642,9 @@ def ep_expert_gemm(x, w, cu_seqlens, y, transpose_w=False, slot_order=None, rep_
     E, N = w.shape[0], w.shape[2 if transpose_w else 1]
     _shape("w", w, *((E, K, N) if transpose_w else (E, N, K)))
     _shape("y", y, rows, N)
-    with _device_of(x, w, y, cu_seqlens, slot_order, rep_expert, dev_status):
-        cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
-        _check("ep_expert_gemm", lib().ep_expert_gemm(_p(x), rows, K, _p(w), E, N, int(bool(transpose_w)), cu, n,
-                                                      order, rep, n_rep, _p(y), _p(dev_status), _s(stream)))
+    cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
+    _launch("ep_expert_gemm", (_at(x), rows, K, _at(w), E, N, bool(transpose_w), cu, n, order, rep, n_rep, _at(y),
+                               _at(dev_status)), stream, x, w, y, cu_seqlens, slot_order, rep_expert, dev_status)
 
 
 def ep_expert_up(x, w, cu_seqlens, h, gu=None, slot_order=None, rep_expert=None, dev_status=None, stream=None):
@@ -647,10 +657,9 @@ def ep_expert_up(x, w, cu_seqlens, h, gu=None, slot_order=None, rep_expert=None,
     _shape("h", h, rows, I)
     if gu is not None:
         _shape("gu", gu, rows, 2 * I)
-    with _device_of(x, w, h, gu, cu_seqlens, slot_order, rep_expert, dev_status):
-        cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
-        _check("ep_expert_up", lib().ep_expert_up(_p(x), rows, H, _p(w), E, I, cu, n, order, rep, n_rep, _p(h),
-                                                  _p(gu), _p(dev_status), _s(stream)))
+    cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
+    _launch("ep_expert_up", (_at(x), rows, H, _at(w), E, I, cu, n, order, rep, n_rep, _at(h), _at(gu),
+                             _at(dev_status)), stream, x, w, h, gu, cu_seqlens, slot_order, rep_expert, dev_status)
 
 
 def ep_expert_up_backward(dy, w2, gu, cu_seqlens, dgu, h=None, slot_order=None, rep_expert=None, dev_status=None,
@@ -665,11 +674,10 @@ def ep_expert_up_backward(dy, w2, gu, cu_seqlens, dgu, h=None, slot_order=None, 
     _shape("dgu", dgu, rows, 2 * I)
     if h is not None:
         _shape("h", h, rows, I)
-    with _device_of(dy, w2, gu, dgu, h, cu_seqlens, slot_order, rep_expert, dev_status):
-        cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
-        _check("ep_expert_up_backward",
-               lib().ep_expert_up_backward(_p(dy), rows, H, _p(w2), E, I, _p(gu), cu, n, order, rep, n_rep, _p(dgu),
-                                           _p(h), _p(dev_status), _s(stream)))
+    cu, n, order, rep, n_rep = _slots(cu_seqlens, slot_order, rep_expert)
+    _launch("ep_expert_up_backward", (_at(dy), rows, H, _at(w2), E, I, _at(gu), cu, n, order, rep, n_rep, _at(dgu),
+                                      _at(h), _at(dev_status)), stream, dy, w2, gu, dgu, h, cu_seqlens, slot_order,
+            rep_expert, dev_status)
 
 
 def _grad_rows(what, g, M, N):
@@ -678,7 +686,7 @@ def _grad_rows(what, g, M, N):
         raise ValueError(f"{what}: expected [n, {M}, {N}] with contiguous rows")
     if not g.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    return ctypes.c_void_p(g.data_ptr()), g.stride(0) if g.shape[0] > 1 else max(g.stride(0), M * N)
+    return g.data_ptr(), g.stride(0) if g.shape[0] > 1 else max(g.stride(0), M * N)
 
 
 def ep_expert_wgrad(a, b, cu_seqlens, g_home, g_rep=None, accumulate=False, slot_order=None, rep_expert=None,
@@ -699,11 +707,10 @@ def ep_expert_wgrad(a, b, cu_seqlens, g_home, g_rep=None, accumulate=False, slot
         rep, ld_rep = _grad_rows("g_rep", g_rep, M, N)
         n_rep = g_rep.shape[0]
         dt = EP_DTYPE_F32 if g_rep.dtype == torch.float32 else EP_DTYPE_BF16
-    with _device_of(a, b, cu_seqlens, g_home, g_rep, slot_order, dev_status):
-        cu, n, order, _, _ = _slots(cu_seqlens, slot_order, None)
-        _check("ep_expert_wgrad",
-               lib().ep_expert_wgrad(_p(a), _p(b), rows, M, N, cu, n, order, home, g_home.shape[0], ld_home, rep, dt,
-                                     n_rep, ld_rep, int(bool(accumulate)), _p(dev_status), _s(stream)))
+    cu, n, order, _, _ = _slots(cu_seqlens, slot_order, None)
+    _launch("ep_expert_wgrad", (_at(a), _at(b), rows, M, N, cu, n, order, home, g_home.shape[0], ld_home, rep, dt,
+                                n_rep, ld_rep, bool(accumulate), _at(dev_status)), stream, a, b, cu_seqlens, g_home,
+            g_rep, slot_order, dev_status)
 
 
 def adamw_table(params, grads, m, v, m_scale=None, v_scale=None, copies=None):
@@ -738,7 +745,7 @@ def adamw_table(params, grads, m, v, m_scale=None, v_scale=None, copies=None):
                 raise ValueError(f"{field} of tensor {i}: {t.numel()} elements, expected {count}")
             if t.device != params[0].device:
                 raise ValueError(f"tensors on {params[0].device} and {t.device}")
-            setattr(table[i], field, _p(t).value)
+            setattr(table[i], field, _at(t) or None)
         table[i].n = n
     return table, 8 if eight else 32, EP_DTYPE_BF16 if gdt == {torch.bfloat16} else EP_DTYPE_F32
 
@@ -756,10 +763,9 @@ def ep_adamw(table, n_tensors, state_bits, grad_dtype, step, lr, betas=(0.9, 0.9
     for name, t in (("step", step), ("lr", lr_dev), ("grad_scale", grad_scale)):
         if t is not None and t.numel() != 1:
             raise ValueError(f"{name}: expected one element")
-    with _device_of(step, lr_dev, grad_scale):
-        _check("ep_adamw", lib().ep_adamw(table, n_tensors, state_bits, grad_dtype, _p(step),
-                                          0.0 if lr_dev is not None else lr, _p(lr_dev), betas[0], betas[1], eps,
-                                          weight_decay, _p(grad_scale), _s(stream)))
+    _launch("ep_adamw", (table, n_tensors, state_bits, grad_dtype, _at(step), 0.0 if lr_dev is not None else lr,
+                         _at(lr_dev), betas[0], betas[1], eps, weight_decay, _at(grad_scale)), stream, step, lr_dev,
+            grad_scale)
 
 
 def ep_selftest_lookback_timeout(topk_ids, E, loads, max_vio, ws, dev_status, stream=None):

@@ -61,11 +61,13 @@ class EpAdamW:
     def step(self, grad_scale=None, stream=None):
         """One step from the gradients as they are now; grad_scale: fp32 CUDA
         tensor of one element that multiplies them (a clipping factor)."""
-        st = stream if stream is not None else torch.cuda.current_stream(self.device)
-        with torch.cuda.stream(st):
+        if stream is None:
             self.steps.add_(1)
+        else:
+            with torch.cuda.stream(stream):
+                self.steps.add_(1)
         ep_adamw(self._table, len(self.params), self.state_bits, self._grad_dtype, self.steps, self.lr, self.betas,
-                 self.eps, self.weight_decay, grad_scale, st)
+                 self.eps, self.weight_decay, grad_scale, stream)
 
     def state_dict(self):
         """The state's own tensors (not copies)."""
