@@ -357,6 +357,28 @@ def test_many_slots_more_than_a_block_of_threads():
 
 
 @gpu
+@pytest.mark.parametrize("n,M,N", [(40, 520, 520), (600, 72, 136), (513, 8, 264), (512, 264, 8)])
+def test_weight_gradients_of_many_slots_of_unlike_length(n, M, N):
+    """More tiles than are at work at once, from slots of 0 to 900 rows, below and above the table that is sorted."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    rng = np.random.default_rng(n)
+    lens = np.minimum(900, rng.geometric(1 / 60, n)) * rng.integers(0, 2, n)
+    lens[n // 2] = 900
+    buf = Buffer([int(v) for v in lens], replicas=False)
+    order = rng.permutation(n).astype(np.int32)
+    a, b = values((buf.P, M), 1, True), values((buf.P, N), 2, True)
+    poison_outside(buf, a, b)
+    g, st = out((n, M, N), dtype=torch.float32), status()
+    tdh.ep_expert_wgrad(a, b, buf.cu[:n + 1], g, slot_order=torch.from_numpy(order).cuda(), dev_status=st)
+    assert tdh.ep_status_read(st) == 0
+    want, _ = wgrad_want(buf, a, b)
+    check(g[torch.from_numpy(order.astype(np.int64)).cuda()], want, torch.zeros_like(want))
+    tdh.ep_expert_wgrad(a, b, buf.cu[:n + 1], g, slot_order=torch.from_numpy(order).cuda(), accumulate=True)
+    check(g[torch.from_numpy(order.astype(np.int64)).cuda()], 2 * want, torch.zeros_like(want))
+
+
+@gpu
 def test_two_streams_and_a_replayed_graph_give_the_same_bits():
     import torch
     import token_dispatch_histogram_b200 as tdh

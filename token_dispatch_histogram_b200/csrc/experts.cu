@@ -71,6 +71,7 @@ constexpr uint32_t A_BYTES = TM / 2 * TK * 2, B_BYTES = TN / 2 * TK * 2;
 constexpr uint32_t RING_BYTES = 12 * A_BYTES;  // 4 stages of an A and two B tiles, or 6 of one each
 constexpr int MAX_STAGES = 6;
 constexpr int TILES_AHEAD = 4;
+constexpr int SORTED_SLOTS = 512;
 constexpr int PART = 8;  // WGRAD: blocks of TK rows that the accumulator sums by itself
 constexpr int MAX_SLOTS = 2 * EP_MAX_EXPERTS + EP_MAX_RANKS - 1;  // E homes and E + R - 1 replicas
 constexpr int BAND = 8;  // tiles of a slot are walked in bands of 8 row blocks, so that the CTAs at work at a
@@ -156,6 +157,7 @@ struct ExpertShared {
   uint32_t tmem;
   int abort;
   int32_t warp_sums[32];
+  uint16_t sorted[SORTED_SLOTS];  // WGRAD: the slots by descending rows
   int32_t before[MAX_SLOTS + 1];  // tiles before each slot
 };
 
@@ -211,7 +213,7 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const ExpertShare
   *hint = lo;
   int32_t ignore = 0;
   Tile r;
-  r.slot = load_slot<F>(a, lo, &ignore);
+  r.slot = load_slot<F>(a, F == WGRAD && a.n_slots <= SORTED_SLOTS ? sh->sorted[lo] : lo, &ignore);
   const int nb = (a.N + halves * tn - 1) / (halves * tn);
   const int mb = ((F == WGRAD ? a.K : r.slot.len) + TM - 1) / TM;
   const int i = t - sh->before[lo];
@@ -407,9 +409,25 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
   if (warp == 2) tmem_alloc(&sh->tmem, 2 * TN);
   int32_t bits = 0;
   {
+    // A weight gradient's tiles take as long as their slot has rows, and a pair takes every so many-th tile: with the
+    // slots by descending rows, and every other round of tiles handed out backwards, all pairs get about the same
+    // (196,608 rows in 64 slots of unlike length: 724 us against 767).  Every CTA finds the same order: ties by the slot.
+    // Ranking each slot against all others is quick up to some hundred slots; longer tables stay as they are.
+    const bool sorted = F == WGRAD && a.n_slots <= SORTED_SLOTS;
+    if (sorted) {
+      for (int s = tid; s < a.n_slots; s += EXP_THREADS) sh->before[s] = load_slot<F>(a, s, &bits).len;
+      __syncthreads();
+      for (int s = tid; s < a.n_slots; s += EXP_THREADS) {
+        const int len = sh->before[s];
+        int r = 0;
+        for (int o = 0; o < a.n_slots; ++o) r += sh->before[o] > len || (sh->before[o] == len && o < s);
+        sh->sorted[r] = (uint16_t)s;
+      }
+      __syncthreads();
+    }
     const int nb = (a.N + halves * tn - 1) / (halves * tn);
     for (int s = tid; s < a.n_slots; s += EXP_THREADS) {
-      const Slot slot = load_slot<F>(a, s, &bits);
+      const Slot slot = load_slot<F>(a, sorted ? sh->sorted[s] : s, &bits);
       const int mb = slot.len < 0 ? 0 : ((F == WGRAD ? a.K : slot.len) + TM - 1) / TM;
       sh->before[s] = F == WGRAD && a.accumulate && slot.len == 0 ? 0 : mb * nb;
     }
@@ -526,12 +544,14 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     // ---- the tiles, a few ahead of the other warps: a search and loads that depend on each other
     int hint = 0, at = 0;
     uint32_t phase = 0;
-    for (int t = first;; t += step) {
+    for (int i = 0;; ++i) {
       if (!wait_warp(&sh->tile_empty[at], phase ^ 1, sh, a.dev_status)) break;
       Tile tile = {};
       tile.steps = -1;
       tile.halves = 1;
+      const int t = i * step + (F == WGRAD && (i & 1) ? step - 1 - first : first);
       if (t < order.wide + order.narrow) tile = find_tile<F>(a, sh, order, t, &hint);
+      else if (F == WGRAD && i * step < order.wide) continue;  // nothing in a last round that is handed out backwards
       if (tile.halves == 0) continue;
       if (lane == 0) {
         sh->tiles[at] = tile;
