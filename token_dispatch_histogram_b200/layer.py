@@ -6,7 +6,11 @@ makes all shapes known in advance: [GR] "Online planning, zero copy και
 sequence of libep.so calls on one stream, with no host synchronisation:
 
   ep_route_fused (= ep_route_stats -> ep_plan -> ep_layout -> ep_align_sort)
-  -> ep_dispatch -> [expert: outside the path] -> ep_combine -> ep_replica_grad_reduce
+  -> ep_dispatch -> [expert] -> ep_combine -> ep_replica_grad_reduce
+
+In front of it router() makes the routing from router logits; between dispatch
+and combine experts() runs the experts' products over the plan's slots, and
+experts_backward() their gradients, the weights' into g_home and g_rep.
 
 `step()` is one pass of that sequence over the resident inputs; `run_host()`
 is the same pass fed from pinned host buffers (copies in, result out),
@@ -15,10 +19,10 @@ Plumbing only: every computation happens in the library's kernels.
 """
 import torch
 
-from . import (align_sort_capacity, ep_align_sort, ep_combine, ep_dispatch, ep_expert_scale, ep_layout,
-               ep_plan, ep_plan_layout, ep_replica_grad_reduce, ep_route_dispatch_fused, ep_route_fused, ep_route_stats,
-               ep_status_read,
-               ep_workspace_size)
+from . import (align_sort_capacity, ep_align_sort, ep_combine, ep_dispatch, ep_expert_gemm, ep_expert_scale,
+               ep_expert_up, ep_expert_up_backward, ep_expert_wgrad, ep_layout, ep_plan, ep_plan_layout,
+               ep_replica_grad_reduce, ep_route_dispatch_fused, ep_route_fused, ep_route_stats, ep_router,
+               ep_status_read, ep_workspace_size)
 
 
 def slice_bounds(T, chunks):
@@ -114,8 +118,54 @@ class EpLayer:
         """y = bf16(buf * s_e) in place (stands in for the grouped GEMM)."""
         ep_expert_scale(self.buf, self.src, self.topk_ids, scale, self.buf, self.dev_status, stream)
 
-    def combine(self, stream=None):
-        ep_combine(self.buf, self.w, self.pos, self.out, self.dev_status, stream)
+    def combine(self, stream=None, y=None):
+        """out = the weighted sum of each token's rows of y (the dispatch
+        buffer itself unless given)."""
+        ep_combine(self.buf if y is None else y, self.w, self.pos, self.out, self.dev_status, stream)
+
+    # --- the model around the path ----------------------------------------
+    def router(self, logits, stream=None, **kw):
+        """topk_ids and w from router logits [T, E]; kw as ep_router's (score,
+        bias, n_group, topk_group, group_top, renorm, scale)."""
+        ep_router(logits, self.topk_ids, self.w, dev_status=self.dev_status, stream=stream, **kw)
+
+    def slots(self):
+        """The plan's slots as the experts' products take them (views of the
+        plan: whatever the last route wrote)."""
+        n = self.E + self.plan_layout["cap"]
+        return dict(cu_seqlens=self.plan_view("cu_seqlens", n + 1), slot_order=self.plan_view("slot_order", n),
+                    rep_expert=self.plan_view("rep_expert", n - self.E))
+
+    def experts(self, w13, w2, h, gu=None, y=None, stream=None):
+        """Rows of the dispatch buffer through their experts: h [P, I] =
+        silu(gate) * up of w13 [E, 2I, H], then w2 [E, H, I] into y.  y=None
+        writes over the dispatch buffer, where combine() reads; for training
+        give a y of its own (w13's gradient needs the dispatched rows) and gu
+        [P, 2I]."""
+        kw = dict(dev_status=self.dev_status, stream=stream, **self.slots())
+        ep_expert_up(self.buf, w13, h=h, gu=gu, **kw)
+        ep_expert_gemm(h, w2, y=self.buf if y is None else y, **kw)
+
+    def weight_grads(self, I):
+        """g_home and g_rep as w13's and w2's gradients ([n, 2I, H] and
+        [n, H, I] each: the two parts of a row; grad_n = 3*H*I)."""
+        H = self.H
+        if self.grad_n != 3 * H * I:
+            raise ValueError(f"grad_n {self.grad_n}, expected 3*H*I = {3 * H * I}")
+        cut = 2 * I * H
+        return [(g[:, :cut].unflatten(1, (2 * I, H)), g[:, cut:].unflatten(1, (H, I))) for g in (self.g_home, self.g_rep)]
+
+    def experts_backward(self, dy, rows, w13, w2, gu, dgu, h, dx, accumulate=False, stream=None):
+        """From dy [P, H]: dgu [P, 2I], h again (both may be overwritten ones of
+        the forward), dx [P, H] (may be dy), and the weights' gradients into
+        g_home and g_rep; rows are the dispatched rows and gu what experts()
+        kept.  grad_reduce() then adds the replicas' to their home's."""
+        kw = dict(dev_status=self.dev_status, stream=stream, **self.slots())
+        (home13, home2), (rep13, rep2) = self.weight_grads(w2.shape[2])
+        ep_expert_up_backward(dy, w2, gu, dgu=dgu, h=h, **kw)
+        ep_expert_wgrad(dy, h, g_home=home2, g_rep=rep2, accumulate=accumulate, **kw)
+        ep_expert_wgrad(dgu, rows, g_home=home13, g_rep=rep13, accumulate=accumulate, **kw)
+        ep_expert_gemm(dgu, w13, y=dx, transpose_w=True, **kw)
 
     def grad_reduce(self, clear=False, stream=None):
         if self.grad_n:

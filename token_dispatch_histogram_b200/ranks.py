@@ -319,6 +319,35 @@ class EpRank:
         ep_combine_peer(self.peers, self.buf_rows, self.R * self.SK, self.w_local, self.pos_local, self.out_local,
                         None, self.rank_first, self.dev_status, stream)
 
+    def slots(self, stream=None):
+        """This rank's slots as the experts' products take them over buf: the
+        whole plan's table with the other ranks' slots left empty, rows from
+        buf's first one, and weight rows of this rank's own table: e - rank*E/R
+        for home expert e, E/R + j for the j-th received replica (its weights in
+        prefetch slot j, its gradient in row j of g_rep).  New tensors, from the
+        plan as it is on the device."""
+        lay, E, R = self.plan_layout, self.E, self.R
+        ER, cap = E // R, self.plan_layout["cap"]
+
+        def view(name, n):
+            return self.plan[lay[name]:lay[name] + n]
+
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+            ids = view("slot_order", E + cap).long()
+            rep = ids - E
+            known = rep.clamp(0, cap - 1)
+            mine_rep = (rep >= 0) & (view("rep_rank", cap)[known] == self.rank)
+            mine_home = (ids >= self.rank * ER) & (ids < (self.rank + 1) * ER)
+            first = view("rank_rep_first", R)[self.rank]
+            order = torch.where(mine_home, ids - self.rank * ER, torch.where(mine_rep, ER + rep - first, -1))
+            cu = view("cu_seqlens", E + cap + 1)
+            if self.rank_first is None:
+                cu = (cu - self.rank * self.SK).clamp_(0, self.SK)
+            else:  # rows past the buffer were not dispatched
+                cu = torch.minimum((cu - self.rank_first[self.rank]).clamp_(0, self.buf_rows),
+                                   view("rank_load", R)[self.rank])
+            return dict(cu_seqlens=cu.to(torch.int32), slot_order=order.to(torch.int32))
+
     def grad_reduce(self, clear=False, stream=None):
         fn = ep_replica_grad_reduce_peer if self.planner == "exact" else ep_quota_replica_grad_reduce_peer
         fn(self.g_home, self.grad_peers, self.rep_rows, self.g_rep.dtype, self.E, self.rank, self.plan, clear,
