@@ -60,10 +60,11 @@
  *    E % R == 0, H % 8 == 0, P < 2^31.
  *  - The row movers (dispatch; combine, which also serves as the backward of
  *    dispatch; the replica gradient reduction; one-buffer and rank-local
- *    forms) are launched with programmatic dependent launch: the GPU may
- *    schedule them while the preceding kernel in the stream finishes, and
- *    each waits for that kernel's completion before touching memory, so
- *    stream order holds as for any launch.
+ *    forms), the router, the experts' products and AdamW are launched with
+ *    programmatic dependent launch: the GPU may schedule them while the
+ *    preceding kernel in the stream finishes, and each waits for that kernel's
+ *    completion before touching memory, so stream order holds as for any
+ *    launch.
  *  - A workspace (ws) holds the counters and grid-barrier words of the call
  *    that uses it: calls in flight at the same time (on different streams)
  *    need workspaces of their own.  Calls on one stream may share one.

@@ -174,9 +174,10 @@ __device__ __forceinline__ float store8_codes(uint8_t* p, int64_t i, int64_t n, 
 }
 
 template <bool EIGHT, bool GRAD_BF16>
-__global__ void __launch_bounds__(ADAM_WARPS * 32)
+__global__ void __launch_bounds__(ADAM_WARPS * 32, 4)
     k_adamw(const __grid_constant__ AdamTable tab, const __grid_constant__ AdamArgs a) {
   __shared__ AdamConst s_c;
+  wait_for_predecessor();
   if (threadIdx.x == 0) s_c = adam_const(a);
   __syncthreads();
   const AdamConst c = s_c;
@@ -275,19 +276,16 @@ extern "C" int ep_adamw(const EpAdamWTensor* tensors, int n_tensors, int state_b
     }
     if (tab.n == 0) break;
     tab.before[tab.n] = (int32_t)blocks;
-    const int64_t want = (blocks + ADAM_WARPS - 1) / ADAM_WARPS, most = (int64_t)num_sms() * 8;
-    const unsigned grid = (unsigned)(want < most ? want : most);
-    if (eight && gb)
-      k_adamw<true, true><<<grid, ADAM_WARPS * 32, 0, stream>>>(tab, a);
-    else if (eight)
-      k_adamw<true, false><<<grid, ADAM_WARPS * 32, 0, stream>>>(tab, a);
-    else if (gb)
-      k_adamw<false, true><<<grid, ADAM_WARPS * 32, 0, stream>>>(tab, a);
-    else
-      k_adamw<false, false><<<grid, ADAM_WARPS * 32, 0, stream>>>(tab, a);
+    // Many short rounds of CTAs rather than one resident grid: 100 M elements in 300 tensors 424 us against 496 with
+    // 8 CTAs an SM in all (and 441 with them at 4 resident), 352 M with 8-bit moments 1047 against 1180
+    const int64_t want = (blocks + ADAM_WARPS - 1) / ADAM_WARPS, most = (int64_t)num_sms() * 128;
+    const void* fn = eight ? gb ? (const void*)k_adamw<true, true> : (const void*)k_adamw<true, false>
+                           : gb ? (const void*)k_adamw<false, true> : (const void*)k_adamw<false, false>;
+    void* args[] = {&tab, (void*)&a};
+    if (launch_pdl(fn, dim3((unsigned)(want < most ? want : most)), dim3(ADAM_WARPS * 32), args, 0, stream) !=
+        cudaSuccess)
+      return EP_ERR_CUDA;
     count_launch();
-    const int rc = launch_status();
-    if (rc != EP_OK) return rc;
   }
   return EP_OK;
 }

@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     fence_mbar_init();
   }
   if (warp == 2) tmem_alloc(&sh->tmem, 2 * TN);
+  wait_for_predecessor();
   int32_t bits = 0;
   {
     // A weight gradient's tiles take as long as their slot has rows, and a pair takes every so many-th tile: with the
@@ -748,9 +749,12 @@ constexpr size_t EXP_SMEM = 1024 + RING_BYTES + sizeof(ExpertShared);
 template <Form F>
 static int launch_experts(const CUtensorMap& ma, const CUtensorMap& mb, const ExpertArgs& a, cudaStream_t stream) {
   if (!raise_smem_limit((const void*)k_experts<F>, EXP_SMEM)) return EP_ERR_CUDA;
-  k_experts<F><<<num_sms() / 2 * 2, EXP_THREADS, EXP_SMEM, stream>>>(ma, mb, a);
+  void* args[] = {(void*)&ma, (void*)&mb, (void*)&a};
+  if (launch_pdl((const void*)k_experts<F>, dim3(num_sms() / 2 * 2), dim3(EXP_THREADS), args, EXP_SMEM, stream) !=
+      cudaSuccess)
+    return EP_ERR_CUDA;
   count_launch();
-  return launch_status();
+  return EP_OK;
 }
 
 // x as tiles of 64 columns and W, rows x cols per expert, along K or along N.

@@ -430,6 +430,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3
   double* mine = s_key + (size_t)warp * a.E;
   RouterList* list = s_list + warp;
   const int width = a.width, batch = 32 / width, of = lane / width, k = lane % width;
+  wait_for_predecessor();
   float b[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -562,6 +563,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32)
 #pragma unroll
   for (int c = 0; c < NC; ++c) *reinterpret_cast<float4*>(out + c * 128 + lane * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncwarp();
+  wait_for_predecessor();
   uint32_t bits = 0;
   const int64_t t0 = ((int64_t)blockIdx.x * ROUTER_WARPS + warp) * batch;
   if (t0 < a.T) {
@@ -694,10 +696,12 @@ static int launch_router(const void* logits, const float* bias, const RouterArgs
   if (!raise_smem_limit((const void*)k_router<V, NV, FULL>, smem)) return EP_ERR_CUDA;
   // one batch a warp, not a resident grid that goes on to the next: 356 against 366 us, with groups 292 against 323
   const int64_t per = ROUTER_WARPS * (32 / a.width);
-  k_router<V, NV, FULL><<<(unsigned)((a.T + per - 1) / per), ROUTER_WARPS * 32, smem, stream>>>((const V*)logits, bias, a,
-                                                                                                ids, w, dev_status);
+  void* args[] = {&logits, &bias, (void*)&a, &ids, &w, &dev_status};
+  if (launch_pdl((const void*)k_router<V, NV, FULL>, dim3((unsigned)((a.T + per - 1) / per)), dim3(ROUTER_WARPS * 32),
+                 args, smem, stream) != cudaSuccess)
+    return EP_ERR_CUDA;
   count_launch();
-  return launch_status();
+  return EP_OK;
 }
 
 template <typename V>
@@ -730,10 +734,12 @@ static int launch_backward(const float* dw, const void* logits, const int32_t* i
   if (!raise_smem_limit((const void*)k_router_backward<V, NC, VEC>, smem)) return EP_ERR_CUDA;
   // one batch a warp: 188 us against 219 with a resident grid (524,288 tokens, 384 experts)
   const int64_t per = ROUTER_WARPS * (32 / a.width);
-  k_router_backward<V, NC, VEC><<<(unsigned)((a.T + per - 1) / per), ROUTER_WARPS * 32, smem, stream>>>(
-      dw, (const V*)logits, ids, a, ld_out, (V*)dlogits, dev_status);
+  void* args[] = {&dw, &logits, &ids, (void*)&a, &ld_out, &dlogits, &dev_status};
+  if (launch_pdl((const void*)k_router_backward<V, NC, VEC>, dim3((unsigned)((a.T + per - 1) / per)),
+                 dim3(ROUTER_WARPS * 32), args, smem, stream) != cudaSuccess)
+    return EP_ERR_CUDA;
   count_launch();
-  return launch_status();
+  return EP_OK;
 }
 
 template <typename V>
