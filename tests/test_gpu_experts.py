@@ -131,6 +131,39 @@ def test_gemm(lens, K, N, transposed, ints):
     check(y, want, rounded(sum_bound(K, mag), want, y.dtype), buf, 7.0)
 
 
+@gpu
+@pytest.mark.parametrize("lens", [[1] * 8, [0, 3, 0, 8, 1, 33, 0, 0, 2, 1, 0, 5], [64] + [0] * 9 + [65] + [0] * 9],
+                         ids=str)
+@pytest.mark.parametrize("K,N", [(8, 8), (72, 264), (200, 136), (1024, 128), (64, 392), (2048, 520)])
+def test_gemm_of_few_rows_a_slot(lens, K, N):
+    """The form for decoding: the average is what decides, and a slot may have more than it takes at a time."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    buf = Buffer(lens, before=1, behind=2)
+    assert buf.P <= 8 * buf.E
+    for ints in (True, False):
+        x, w = values((buf.P, K), 1, ints), values((buf.E, N, K), 2, ints)
+        poison_outside(buf, x)
+        y, st = out((buf.P, N)), status()
+        tdh.ep_expert_gemm(x, w, buf.cu, y, dev_status=st, **buf.kw)
+        want, mag = product(buf, x, w, False)
+        if ints:
+            check(y, want.to(torch.bfloat16).double(), torch.zeros_like(want), buf, 7.0)
+        check(y, want, rounded(sum_bound(K, mag), want, y.dtype), buf, 7.0)
+        if N % 16 == 0 and not ints:
+            I = N // 2
+            h, gu = out((buf.P, I)), out((buf.P, N))
+            tdh.ep_expert_up(x, w, buf.cu, h, gu, dev_status=st, **buf.kw)
+            check(gu, want, rounded(sum_bound(K, mag), want, gu.dtype), buf, 7.0)
+            g, u = want[:, :I], want[:, I:]
+            e = sum_bound(K, mag)
+            act = silu(g) * u
+            bound = (1.1 * e[:, :I] * (u.abs() + e[:, I:]) + (silu(g).abs() + 1.1 * e[:, :I]) * e[:, I:]
+                     + act.abs() * (g.abs() + 16) * 2.0 ** -22)
+            check(h, act, rounded(bound, act, h.dtype), buf, 7.0)
+        assert tdh.ep_status_read(st) == 0
+
+
 def silu(g):
     import torch
     return g * torch.sigmoid(g)

@@ -746,6 +746,233 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
 
 constexpr size_t EXP_SMEM = 1024 + RING_BYTES + sizeof(ExpertShared);
 
+// ---------------------------------------------------------------- few rows
+//
+// Decoding: a few rows to a slot, the time is that of reading the weights.  The
+// tiles above would multiply 256 rows for the sake of three (at 192 rows over 64
+// experts, H 2048, I 1024, up: 104 us, the weights alone 82).  Here the weights are
+// the operand with 128 rows and up to 32 of the slot's rows are the columns: a
+// product of 128 x 32, and a tile is two of them (UP: 128 rows of the gate and of
+// the up projection; otherwise 256 rows of W) with fresh weights for nearly all of
+// what is loaded (90 us there).  One CTA to a tile, 160 KB of weights on the way to
+// each SM.
+constexpr int FEW = 32;  // rows of a slot to a tile
+constexpr int FEW_THREADS = 256, FEW_STAGES = 5;
+constexpr uint32_t FEW_W = 128 * TK * 2, FEW_X = FEW * TK * 2, FEW_STAGE = 2 * FEW_W + FEW_X;
+
+struct FewShared {
+  uint64_t full[FEW_STAGES], empty[FEW_STAGES], acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  int abort;
+  int32_t warp_sums[32];
+  int32_t before[MAX_SLOTS + 1];
+};
+
+constexpr size_t FEW_SMEM = 1024 + FEW_STAGES * FEW_STAGE + sizeof(FewShared);
+
+// Same walk in every role (tiles are few): the slot by bisection, then its blocks of rows, the weights' blocks outermost.
+template <Form F>
+__device__ __forceinline__ Tile find_few(const ExpertArgs& a, const FewShared* sh, int t, int* hint) {
+  int lo = *hint, hi = a.n_slots - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sh->before[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  *hint = lo;
+  int32_t ignore = 0;
+  Tile r;
+  r.slot = load_slot<F>(a, lo, &ignore);
+  const int mb = (r.slot.len + FEW - 1) / FEW, i = t - sh->before[lo];
+  r.n = i / mb * (F == UP ? 128 : 256);
+  r.m = i % mb * FEW;
+  r.halves = F == UP || r.n + 128 < a.N ? 2 : 1;
+  r.steps = (a.K + TK - 1) / TK;
+  return r;
+}
+
+__device__ __forceinline__ bool wait_few(uint64_t* bar, uint32_t parity, FewShared* sh, int32_t* dev_status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*(volatile int*)&sh->abort) return false;
+    if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+      *(volatile int*)&sh->abort = 1;
+      flag(dev_status, EP_DEV_COPY_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+template <Form F>
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+    k_experts_few(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                  const __grid_constant__ ExpertArgs a) {
+  static_assert(F == UP || F == Y_NT, "");
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
+  FewShared* sh = reinterpret_cast<FewShared*>(ring + FEW_STAGES * FEW_STAGE);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int tn = F == UP ? 128 : 256;
+
+  if (tid == 0) {
+    for (int i = 0; i < FEW_STAGES; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->acc_full[i], 1);
+      mbar_init(&sh->acc_empty[i], 4);
+    }
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc_alone(&sh->tmem, 4 * FEW);  // two tiles' accumulators
+  wait_for_predecessor();
+  int32_t bits = 0;
+  {
+    const int nb = (a.N + tn - 1) / tn;
+    for (int s = tid; s < a.n_slots; s += FEW_THREADS) {
+      const Slot slot = load_slot<F>(a, s, &bits);
+      sh->before[s] = slot.len <= 0 ? 0 : (slot.len + FEW - 1) / FEW * nb;
+    }
+  }
+  if (bits && blockIdx.x == 0) flag(a.dev_status, bits);
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  const int total = block_scan_array(sh->before, a.n_slots, sh->warp_sums);
+  const uint32_t tmem = sh->tmem;
+
+  if (tid == 0) {
+    int stage = 0, hint = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const Tile tile = find_few<F>(a, sh, t, &hint);
+      for (int k = 0; k < tile.steps; ++k) {
+        if (!(ok = wait_few(&sh->empty[stage], phase ^ 1, sh, a.dev_status))) break;
+        uint8_t* s = ring + stage * FEW_STAGE;
+        uint64_t* bar = &sh->full[stage];
+        mbar_arrive_expect_tx(bar, tile.halves * FEW_W + FEW_X);
+        const int kk = k * TK;
+        tma_tile_3d_alone(s, &map_w, bar, kk, tile.n, tile.slot.w);
+        if (tile.halves == 2)
+          tma_tile_3d_alone(s + FEW_W, &map_w, bar, kk, F == UP ? a.N + tile.n : tile.n + 128, tile.slot.w);
+        tma_tile_2d_alone(s + 2 * FEW_W, &map_x, bar, kk, (int)tile.slot.begin + tile.m);
+        if (++stage == FEW_STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (tid == 32) {
+    constexpr uint32_t idesc = umma_idesc(128, FEW, false, false);
+    int stage = 0, hint = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const Tile tile = find_few<F>(a, sh, t, &hint);
+      if (!(ok = wait_few(&sh->acc_empty[acc], acc_phase ^ 1, sh, a.dev_status))) break;
+      for (int k = 0; k < tile.steps; ++k) {
+        if (!(ok = wait_few(&sh->full[stage], phase, sh, a.dev_status))) break;
+        umma_fence_after();
+        const uint32_t s = smem_addr(ring + stage * FEW_STAGE);
+        const uint64_t dx = umma_smem_desc(s + 2 * FEW_W, 16, 1024);
+        for (int h = 0; h < tile.halves; ++h) {
+          const uint64_t dw = umma_smem_desc(s + h * FEW_W, 16, 1024);
+#pragma unroll
+          for (int i = 0; i < TK / 16; ++i)
+            umma_bf16_alone(tmem + (2 * acc + h) * FEW, dw + i * 2, dx + i * 2, idesc, k > 0 || i > 0);
+        }
+        umma_commit_alone(&sh->empty[stage]);
+        if (++stage == FEW_STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) umma_commit_alone(&sh->acc_full[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  } else if (warp >= 4) {
+    // lane = column of the result: 32 neighbouring columns of a row go out together
+    const int col = (warp - 4) * 32 + lane;
+    int hint = 0, acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      const Tile tile = find_few<F>(a, sh, t, &hint);
+      if (!__all_sync(0xffffffffu, wait_few(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
+      umma_fence_after();
+      const uint32_t src = tmem + ((uint32_t)(warp - 4) << 21) + 2 * acc * FEW;
+      uint32_t r[2][FEW];
+      tmem_load(src, r[0]);
+      tmem_load(src + FEW, r[1]);  // not written where the tile has one half; then it is not used either
+      tmem_wait_load(r[0]);
+      tmem_wait_load(r[1]);
+      umma_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+      const int rows = tile.slot.len - tile.m, n = tile.n + col;
+      const int64_t at = tile.slot.begin + tile.m;
+#pragma unroll
+      for (int i = 0; i < FEW; ++i) {
+        if (i >= rows) break;
+        const float v = __uint_as_float(r[0][i]), u = __uint_as_float(r[1][i]);
+        if (F == UP) {
+          if (n < a.N) {
+            a.y[(at + i) * a.N + n] = (uint16_t)f32x2_to_bf16x2(v * sigmoid_fast(v) * u, 0.f);
+            if (a.y2) {
+              uint16_t* gu = a.y2 + (at + i) * 2 * a.N + n;
+              gu[0] = (uint16_t)f32x2_to_bf16x2(v, 0.f);
+              gu[a.N] = (uint16_t)f32x2_to_bf16x2(u, 0.f);
+            }
+          }
+        } else {
+          if (n < a.N) a.y[(at + i) * a.N + n] = (uint16_t)f32x2_to_bf16x2(v, 0.f);
+          if (n + 128 < a.N) a.y[(at + i) * a.N + n + 128] = (uint16_t)f32x2_to_bf16x2(u, 0.f);
+        }
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+  __syncwarp();
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  if (sh->abort && tid == 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < WAIT_LIMIT_NS / 10) {
+    }
+  }
+  __syncthreads();
+  if (warp == 2) tmem_free_alone(tmem, 4 * FEW);
+}
+
+template <Form F>
+static int launch_few(const CUtensorMap& mx, const CUtensorMap& mw, const ExpertArgs& a, cudaStream_t stream) {
+  if (!raise_smem_limit((const void*)k_experts_few<F>, FEW_SMEM)) return EP_ERR_CUDA;
+  void* args[] = {(void*)&mx, (void*)&mw, (void*)&a};
+  if (launch_pdl((const void*)k_experts_few<F>, dim3(num_sms()), dim3(FEW_THREADS), args, FEW_SMEM, stream) !=
+      cudaSuccess)
+    return EP_ERR_CUDA;
+  count_launch();
+  return EP_OK;
+}
+
+// Few rows to a slot on average: then the weights' bytes are what counts.  Up over 64 experts (H 2048, I 1024), us wide /
+// few: 8 rows a slot 106 / 93, 32 rows 109 / 94, 64 rows 112 / 139.  But the host knows the average only; with all rows in
+// one slot: 8 a slot 26 / 26, 16 a slot 29 / 49, 32 a slot 27 / 78.  Up to 8 it never costs.
+static bool few_rows(int64_t rows, int n_slots, int n_w) { return rows <= 8 * (int64_t)(n_slots < n_w ? n_slots : n_w); }
+
 template <Form F>
 static int launch_experts(const CUtensorMap& ma, const CUtensorMap& mb, const ExpertArgs& a, cudaStream_t stream) {
   if (!raise_smem_limit((const void*)k_experts<F>, EXP_SMEM)) return EP_ERR_CUDA;
@@ -802,6 +1029,10 @@ extern "C" int ep_expert_gemm(const uint16_t* x, int64_t rows, int64_t K, const 
   a.rows = rows, a.N = (int)N, a.K = (int)K, a.n_slots = n_slots, a.n_w = n_w, a.n_rep = rep_expert ? n_rep : 0;
   a.cu = cu_seqlens, a.slots = slot_order, a.rep = rep_expert, a.y = y, a.dev_status = dev_status;
   CUtensorMap ma, mb;
+  if (!transpose_w && few_rows(rows, n_slots, n_w)) {
+    if (!map_rows(&ma, x, rows, (int)K, FEW) || !map_weights(&mb, w, n_w, (int)N, (int)K, 128)) return EP_ERR_CUDA;
+    return launch_few<Y_NT>(ma, mb, a, stream);
+  }
   if (!map_rows(&ma, x, rows, (int)K, TM / 2)) return EP_ERR_CUDA;
   if (transpose_w) {
     if (!map_weights(&mb, w, n_w, (int)K, (int)N, TK)) return EP_ERR_CUDA;
@@ -823,8 +1054,12 @@ extern "C" int ep_expert_up(const uint16_t* x, int64_t rows, int64_t H, const ui
   a.rows = rows, a.N = (int)I, a.K = (int)H, a.n_slots = n_slots, a.n_w = n_w, a.n_rep = rep_expert ? n_rep : 0;
   a.cu = cu_seqlens, a.slots = slot_order, a.rep = rep_expert, a.y = h, a.y2 = gu, a.dev_status = dev_status;
   CUtensorMap ma, mb;
-  if (!map_rows(&ma, x, rows, (int)H, TM / 2) || !map_weights(&mb, w, n_w, (int)(2 * I), (int)H, TN / 2))
-    return EP_ERR_CUDA;
+  if (!map_weights(&mb, w, n_w, (int)(2 * I), (int)H, 128)) return EP_ERR_CUDA;
+  if (few_rows(rows, n_slots, n_w)) {
+    if (!map_rows(&ma, x, rows, (int)H, FEW)) return EP_ERR_CUDA;
+    return launch_few<UP>(ma, mb, a, stream);
+  }
+  if (!map_rows(&ma, x, rows, (int)H, TM / 2)) return EP_ERR_CUDA;
   return launch_experts<UP>(ma, mb, a, stream);
 }
 
