@@ -652,7 +652,8 @@ EP_API int ep_route_stats_noalloc(const int32_t* topk_ids, int64_t T, int K, int
  *   topk_ids [T, K] int32 out, w [T, K] fp32 out.
  * A logit of -inf masks its expert: s_e = 0, taken only after every expert that
  * is not masked.  A row of -inf gets the K lowest ids and w = 0.  NaN counts as
- * -inf and +inf as the largest finite fp32; both set EP_DEV_BAD_LOGIT.
+ * -inf and +inf as the largest finite fp32; both set EP_DEV_BAD_LOGIT.  A bias of
+ * -inf or NaN excludes its expert likewise (its score stays).
  * logits, topk_ids, w and bias need the alignment of their element type only.
  * EP_ERR_ARG: a bad shape or type, E % n_group, n_group > 32, topk_group outside
  * [1, n_group] or holding fewer than K experts, group_top other than 1 or 2.
@@ -737,7 +738,9 @@ EP_API int ep_expert_up_backward(const uint16_t* dy, int64_t rows, int64_t H, co
  *   rep_dtype   of g_rep, EP_DTYPE_F32 or EP_DTYPE_BF16.
  *   accumulate  != 0: added to what is there (one fp32 add; bf16 rows rounded
  *               again); otherwise written, zeros for a slot without rows.
- * Rows that belong to no slot are left as they are.  ld_home and ld_rep are at
+ * Rows of g_home and g_rep that belong to no slot are left as they are.  An id that
+ * stands at two slots has no row of its own: both are left out, with
+ * EP_DEV_BAD_EXPERT_ID.  ld_home and ld_rep are at
  * least M * N and keep 16-byte alignment.
  */
 EP_API int ep_expert_wgrad(const uint16_t* a, const uint16_t* b, int64_t rows, int64_t M, int64_t N,

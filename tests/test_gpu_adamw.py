@@ -386,6 +386,8 @@ def test_adamw_refuses_wrong_tensors():
         EpAdamW([x], [x], state_bits=16)
     with pytest.raises(ValueError):
         EpAdamW([x], [x, x])
+    with pytest.raises(ValueError):
+        EpAdamW([x, x], [x, x])
     with pytest.raises(TypeError):
         EpAdamW([x], [x.half()])
     with pytest.raises(ValueError):

@@ -348,6 +348,24 @@ def test_slots_that_do_not_fit_are_left_out_and_flagged():
 
 
 @gpu
+@pytest.mark.parametrize("n", [6, 700])
+def test_an_id_at_two_slots_has_no_gradient_row(n):
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    buf = Buffer([20, 0, 70, 3, 64, 1] + [1] * (n - 6), replicas=False)
+    a, b = values((buf.P, 72), 1, True), values((buf.P, 40), 2, True)
+    order = np.arange(n, dtype=np.int32)
+    order[4] = 2
+    g, st = out((n, 72, 40), dtype=torch.float32), status()
+    tdh.ep_expert_wgrad(a, b, buf.cu[:n + 1], g, slot_order=torch.from_numpy(order).cuda(), dev_status=st)
+    assert tdh.ep_status_read(st) == tdh.EP_DEV_BAD_EXPERT_ID
+    want, _ = wgrad_want(buf, a, b)
+    assert torch.all(g[[2, 4]] == 7.0)
+    rest = [e for e in range(n) if e not in (2, 4)]
+    check(g[rest], want[rest], torch.zeros_like(want[rest]))
+
+
+@gpu
 def test_no_rows_and_no_slots():
     import torch
     import token_dispatch_histogram_b200 as tdh

@@ -233,6 +233,32 @@ def test_nan_and_infinite_logits_are_flagged_and_defined():
 
 
 @gpu
+@pytest.mark.parametrize("E", [20, 64, 1000])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_that_are_not_finite_exclude_or_prefer(score, groups, E):
+    """-inf and NaN exclude their experts (taken last, by index), +inf puts its expert first."""
+    import torch
+    T, K = 40, 8
+    x = logits_of(T, E, torch.float32, 6)
+    bias = (0.1 * np.random.default_rng(1).standard_normal(E)).astype(np.float32)
+    bias[[1, 7]], bias[[2, 11]], bias[5] = -np.inf, np.nan, np.inf
+    kw = dict(score=score, n_group=groups[0], topk_group=groups[1], group_top=groups[2])
+    ids, w, st = call(x.cuda(), K, bias=bias, **kw)
+    want_ids, want = ref_router(x.double().numpy(), K, bias=np.where(np.isnan(bias), -np.inf, bias).astype(np.float64), **kw)
+    assert st == 0 and np.all(ids[:, 0] == 5)
+    if E > 20 or groups[0] == 1:  # two groups of five experts are too few without those excluded
+        assert not np.any(np.isin(ids, [1, 2, 7, 11]))
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(x.double().numpy(), want, ids, 1.0))
+    if groups[0] == 1:
+        bias[:] = np.nan  # nothing left to prefer: by index
+        ids, w, st = call(x.cuda(), K, bias=bias, **kw)
+        np.testing.assert_array_equal(ids, np.tile(np.arange(K), (T, 1)))
+        assert np.all(np.isfinite(w))
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_rows_of_a_wider_matrix(dtype):
     """Any row stride and any start: the logits as columns of a wider projection, outputs into slices."""

@@ -102,6 +102,7 @@ struct ExpertArgs {
   void* g_rep;
   int64_t ld_home, ld_rep;  // elements between experts
   bool rep_bf16, accumulate;
+  uint64_t wait_ns;  // the bound of a wait: a second, and more where a tile may take long
   int32_t* dev_status;
 };
 
@@ -158,18 +159,19 @@ struct ExpertShared {
   int abort;
   int32_t warp_sums[32];
   uint16_t sorted[SORTED_SLOTS];  // WGRAD: the slots by descending rows
+  uint32_t seen[(MAX_SLOTS + 31) / 32], twice[(MAX_SLOTS + 31) / 32];  // WGRAD: ids, and those that stand twice
   int32_t before[MAX_SLOTS + 1];  // tiles before each slot
 };
 
 // A thread's bounded wait, that gives up as soon as another role of the CTA has.
-__device__ __forceinline__ bool wait_thread(uint64_t* bar, uint32_t parity, ExpertShared* sh, int32_t* dev_status) {
+__device__ __forceinline__ bool wait_thread(uint64_t* bar, uint32_t parity, ExpertShared* sh, const ExpertArgs& a) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (*(volatile int*)&sh->abort) return false;
-    if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+    if (globaltimer_ns() - t0 > a.wait_ns) {
       *(volatile int*)&sh->abort = 1;
-      flag(dev_status, EP_DEV_COPY_TIMEOUT);
+      flag(a.dev_status, EP_DEV_COPY_TIMEOUT);
       return false;
     }
   }
@@ -177,8 +179,8 @@ __device__ __forceinline__ bool wait_thread(uint64_t* bar, uint32_t parity, Expe
 }
 
 // The same for a whole warp, with one outcome.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, ExpertShared* sh, int32_t* dev_status) {
-  return __all_sync(0xffffffffu, wait_thread(bar, parity, sh, dev_status));
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, ExpertShared* sh, const ExpertArgs& a) {
+  return __all_sync(0xffffffffu, wait_thread(bar, parity, sh, a));
 }
 
 // The order of a pair's work: `wide` tiles of all the columns a tile can take,
@@ -231,18 +233,18 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& a, const ExpertShare
 template <bool WARP>
 struct Walk {
   ExpertShared* sh;
-  int32_t* dev_status;
+  const ExpertArgs& a;
   int at;
   uint32_t phase;
   Tile tile;
-  __device__ __forceinline__ Walk(ExpertShared* s, int32_t* st) : sh(s), dev_status(st), at(0), phase(0) {}
+  __device__ __forceinline__ Walk(ExpertShared* s, const ExpertArgs& args) : sh(s), a(args), at(0), phase(0) {}
   __device__ __forceinline__ bool next() {
     if (WARP) {
-      if (!wait_warp(&sh->tile_full[at], phase, sh, dev_status)) return false;
+      if (!wait_warp(&sh->tile_full[at], phase, sh, a)) return false;
       tile = sh->tiles[at];
       __syncwarp();
     } else {
-      if (!wait_thread(&sh->tile_full[at], phase, sh, dev_status)) return false;
+      if (!wait_thread(&sh->tile_full[at], phase, sh, a)) return false;
       tile = sh->tiles[at];
     }
     if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&sh->tile_empty[at]);
@@ -415,6 +417,17 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     // (196,608 rows in 64 slots of unlike length: 724 us against 767).  Every CTA finds the same order: ties by the slot.
     // Ranking each slot against all others is quick up to some hundred slots; longer tables stay as they are.
     const bool sorted = F == WGRAD && a.n_slots <= SORTED_SLOTS;
+    if (F == WGRAD) {
+      for (int i = tid; i < (MAX_SLOTS + 31) / 32; i += EXP_THREADS) sh->seen[i] = sh->twice[i] = 0;
+      __syncthreads();
+      for (int s = tid; s < a.n_slots; s += EXP_THREADS) {
+        const Slot slot = load_slot<F>(a, s, &bits);
+        if (slot.len < 0) continue;
+        const uint32_t bit = 1u << (slot.w & 31);
+        if (atomicOr(&sh->seen[slot.w >> 5], bit) & bit) atomicOr(&sh->twice[slot.w >> 5], bit);
+      }
+      __syncthreads();
+    }
     if (sorted) {
       for (int s = tid; s < a.n_slots; s += EXP_THREADS) sh->before[s] = load_slot<F>(a, s, &bits).len;
       __syncthreads();
@@ -429,7 +442,11 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     const int nb = (a.N + halves * tn - 1) / (halves * tn);
     for (int s = tid; s < a.n_slots; s += EXP_THREADS) {
       const Slot slot = load_slot<F>(a, sorted ? sh->sorted[s] : s, &bits);
-      const int mb = slot.len < 0 ? 0 : ((F == WGRAD ? a.K : slot.len) + TM - 1) / TM;
+      int mb = slot.len < 0 ? 0 : ((F == WGRAD ? a.K : slot.len) + TM - 1) / TM;
+      if (F == WGRAD && mb && (sh->twice[slot.w >> 5] >> (slot.w & 31) & 1)) {
+        bits |= EP_DEV_BAD_EXPERT_ID;
+        mb = 0;
+      }
       sh->before[s] = F == WGRAD && a.accumulate && slot.len == 0 ? 0 : mb * nb;
     }
   }
@@ -447,14 +464,14 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    Walk<false> walk(sh, a.dev_status);
+    Walk<false> walk(sh, a);
     while (ok && walk.next()) {
       const Tile& tile = walk.tile;
       // rows behind the slot's end need not be read where a whole half is
       const bool rows = F == WGRAD || tile.m + rank * (TM / 2) < tile.slot.len;
       const uint32_t bytes = tile.halves * B_BYTES + (rows ? A_BYTES : 0);
       for (int k = 0; k < tile.steps; ++k) {
-        if (!(ok = wait_thread(&sh->empty[stage], phase ^ 1, sh, a.dev_status))) break;
+        if (!(ok = wait_thread(&sh->empty[stage], phase ^ 1, sh, a))) break;
         uint8_t* sa = ring + stage * stage_bytes;
         uint8_t* sb = sa + A_BYTES;
         const int kk = k * TK;
@@ -500,15 +517,15 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    Walk<false> walk(sh, a.dev_status);
+    Walk<false> walk(sh, a);
     while (ok && walk.next()) {
       const Tile& tile = walk.tile;
       const bool two = halves == 2 && tile.halves == 2;
       for (int k = 0; k < tile.steps; ++k) {
         const int part = F == WGRAD ? k % PART : k;
         const bool last = k + 1 == tile.steps || (F == WGRAD && part + 1 == PART);
-        if (part == 0 && !(ok = wait_thread(&sh->acc_empty[acc], acc_phase ^ 1, sh, a.dev_status))) break;
-        if (!(ok = wait_thread(&sh->full[stage], phase, sh, a.dev_status))) break;
+        if (part == 0 && !(ok = wait_thread(&sh->acc_empty[acc], acc_phase ^ 1, sh, a))) break;
+        if (!(ok = wait_thread(&sh->full[stage], phase, sh, a))) break;
         umma_fence_after();
         const uint64_t da = da0 + (uint32_t)stage * (stage_bytes >> 4), db = db0 + (uint32_t)stage * (stage_bytes >> 4);
 #pragma unroll
@@ -519,7 +536,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
         if (two) {
           // the next accumulator, which may be the first of its round
           if (part == 0) {
-            if (!(ok = wait_thread(&sh->acc_empty[acc ^ 1], acc_phase ^ 1 ^ acc, sh, a.dev_status))) break;
+            if (!(ok = wait_thread(&sh->acc_empty[acc ^ 1], acc_phase ^ 1 ^ acc, sh, a))) break;
             umma_fence_after();
           }
 #pragma unroll
@@ -546,7 +563,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     int hint = 0, at = 0;
     uint32_t phase = 0;
     for (int i = 0;; ++i) {
-      if (!wait_warp(&sh->tile_empty[at], phase ^ 1, sh, a.dev_status)) break;
+      if (!wait_warp(&sh->tile_empty[at], phase ^ 1, sh, a)) break;
       Tile tile = {};
       tile.steps = -1;
       tile.halves = 1;
@@ -569,14 +586,14 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     // ---- zero the lines behind a slot's end in its last block of rows
     int block = 0;  // blocks of rows so far, modulo the stages
     uint32_t phases = 0;
-    Walk<true> walk(sh, a.dev_status);
+    Walk<true> walk(sh, a);
     while (walk.next()) {
       const Tile& tile = walk.tile;
       block = (block + tile.steps) % stages;
       const int valid = tile.slot.len % TK;
       if (valid == 0) continue;
       const int stage = (block + stages - 1) % stages;
-      if (!wait_warp(&sh->tail[stage], phases >> stage & 1, sh, a.dev_status)) break;
+      if (!wait_warp(&sh->tail[stage], phases >> stage & 1, sh, a)) break;
       phases ^= 1u << stage;
       uint8_t* s = ring + stage * stage_bytes;
       for (int i = lane; i < (TK - valid) * 8; i += 32) {
@@ -597,7 +614,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    Walk<true> walk(sh, a.dev_status);
+    Walk<true> walk(sh, a);
     while (ok && walk.next()) {
       const Tile& tile = walk.tile;
       const int m = tile.m + rank * (TM / 2) + row;
@@ -607,7 +624,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
         for (int i = 0; i < TN / 2; ++i) sum[i] = 0.f;
         for (int k = 0; k < tile.steps; k += PART) {
-          if (!(ok = wait_warp(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
+          if (!(ok = wait_warp(&sh->acc_full[acc], acc_phase, sh, a))) break;
           umma_fence_after();
 #pragma unroll
           for (int c = 0; c < TN / 2; c += 16) {
@@ -643,7 +660,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
             fetch_rows(turn, g, a.gu + at * 2 * a.N + n, 2 * a.N, rows, a.N - n);
             fetch_rows(turn, w, a.gu + at * 2 * a.N + a.N + n, 2 * a.N, rows, a.N - n);
           }
-          if (!(ok = wait_warp(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
+          if (!(ok = wait_warp(&sh->acc_full[acc], acc_phase, sh, a))) break;
           umma_fence_after();
           if (!any) {
             __syncwarp();
@@ -793,14 +810,14 @@ __device__ __forceinline__ Tile find_few(const ExpertArgs& a, const FewShared* s
   return r;
 }
 
-__device__ __forceinline__ bool wait_few(uint64_t* bar, uint32_t parity, FewShared* sh, int32_t* dev_status) {
+__device__ __forceinline__ bool wait_few(uint64_t* bar, uint32_t parity, FewShared* sh, const ExpertArgs& a) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (*(volatile int*)&sh->abort) return false;
-    if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+    if (globaltimer_ns() - t0 > a.wait_ns) {
       *(volatile int*)&sh->abort = 1;
-      flag(dev_status, EP_DEV_COPY_TIMEOUT);
+      flag(a.dev_status, EP_DEV_COPY_TIMEOUT);
       return false;
     }
   }
@@ -854,7 +871,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile tile = find_few<F>(a, sh, t, &hint);
       for (int k = 0; k < tile.steps; ++k) {
-        if (!(ok = wait_few(&sh->empty[stage], phase ^ 1, sh, a.dev_status))) break;
+        if (!(ok = wait_few(&sh->empty[stage], phase ^ 1, sh, a))) break;
         uint8_t* s = ring + stage * FEW_STAGE;
         uint64_t* bar = &sh->full[stage];
         mbar_arrive_expect_tx(bar, tile.halves * FEW_W + FEW_X);
@@ -876,9 +893,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     bool ok = true;
     for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile tile = find_few<F>(a, sh, t, &hint);
-      if (!(ok = wait_few(&sh->acc_empty[acc], acc_phase ^ 1, sh, a.dev_status))) break;
+      if (!(ok = wait_few(&sh->acc_empty[acc], acc_phase ^ 1, sh, a))) break;
       for (int k = 0; k < tile.steps; ++k) {
-        if (!(ok = wait_few(&sh->full[stage], phase, sh, a.dev_status))) break;
+        if (!(ok = wait_few(&sh->full[stage], phase, sh, a))) break;
         umma_fence_after();
         const uint32_t s = smem_addr(ring + stage * FEW_STAGE);
         const uint64_t dx = umma_smem_desc(s + 2 * FEW_W, 16, 1024);
@@ -907,7 +924,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     uint32_t acc_phase = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
       const Tile tile = find_few<F>(a, sh, t, &hint);
-      if (!__all_sync(0xffffffffu, wait_few(&sh->acc_full[acc], acc_phase, sh, a.dev_status))) break;
+      if (!__all_sync(0xffffffffu, wait_few(&sh->acc_full[acc], acc_phase, sh, a))) break;
       umma_fence_after();
       const uint32_t src = tmem + ((uint32_t)(warp - 4) << 21) + 2 * acc * FEW;
       uint32_t r[2][FEW];
@@ -957,8 +974,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   if (warp == 2) tmem_free_alone(tmem, 4 * FEW);
 }
 
+// A warp may wait for as long as a tile takes, and a slot of the weight gradient may have a thousand million rows: 2 us
+// for each block of the contraction (64 KB, at most 0.8 us where all SMs read from HBM) on top of a second.
 template <Form F>
-static int launch_few(const CUtensorMap& mx, const CUtensorMap& mw, const ExpertArgs& a, cudaStream_t stream) {
+static uint64_t wait_bound(const ExpertArgs& a) {
+  return WAIT_LIMIT_NS + (uint64_t)(F == WGRAD ? a.rows : (int64_t)a.K) / TK * 2000;
+}
+
+template <Form F>
+static int launch_few(const CUtensorMap& mx, const CUtensorMap& mw, ExpertArgs a, cudaStream_t stream) {
+  a.wait_ns = wait_bound<F>(a);
   if (!raise_smem_limit((const void*)k_experts_few<F>, FEW_SMEM)) return EP_ERR_CUDA;
   void* args[] = {(void*)&mx, (void*)&mw, (void*)&a};
   if (launch_pdl((const void*)k_experts_few<F>, dim3(num_sms()), dim3(FEW_THREADS), args, FEW_SMEM, stream) !=
@@ -974,7 +999,8 @@ static int launch_few(const CUtensorMap& mx, const CUtensorMap& mw, const Expert
 static bool few_rows(int64_t rows, int n_slots, int n_w) { return rows <= 8 * (int64_t)(n_slots < n_w ? n_slots : n_w); }
 
 template <Form F>
-static int launch_experts(const CUtensorMap& ma, const CUtensorMap& mb, const ExpertArgs& a, cudaStream_t stream) {
+static int launch_experts(const CUtensorMap& ma, const CUtensorMap& mb, ExpertArgs a, cudaStream_t stream) {
+  a.wait_ns = wait_bound<F>(a);
   if (!raise_smem_limit((const void*)k_experts<F>, EXP_SMEM)) return EP_ERR_CUDA;
   void* args[] = {(void*)&ma, (void*)&mb, (void*)&a};
   if (launch_pdl((const void*)k_experts<F>, dim3(num_sms() / 2 * 2), dim3(EXP_THREADS), args, EXP_SMEM, stream) !=

@@ -48,6 +48,9 @@ __device__ __forceinline__ float clean_logit(float x, bool& bad) {
   return x > 0.f ? FLT_MAX : -INFINITY;
 }
 
+// A NaN among the biases excludes its expert as -inf does: a key is never NaN.
+__device__ __forceinline__ float clean_bias(float b) { return b == b ? b : -INFINITY; }
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
@@ -157,7 +160,7 @@ __device__ int select_exact(const RouterArgs& a, const V* __restrict__ row, cons
         k = 1.0 / (1.0 + exp(-x));
       else
         k = exp(x) / (1.0 + exp(x));
-      if (bias) k += (double)bias[e];
+      if (bias) k += (double)clean_bias(bias[e]);
     }
     key[e] = k;
   }
@@ -318,7 +321,7 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       key[j] = a.sigmoid ? rcp_approx(1.f + ex2_approx(x[j] * -LOG2E)) : key[j] * iz;
-      if (bias) key[j] += NV <= HOISTED ? b[j] : FULL || lane + 32 * j < a.E ? bias[lane + 32 * j] : 0.f;
+      if (bias) key[j] += NV <= HOISTED ? b[j] : FULL || lane + 32 * j < a.E ? clean_bias(bias[lane + 32 * j]) : 0.f;
     }
     if (masked) {
 #pragma unroll
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3
   float b[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    b[j] = NV <= HOISTED && bias && (FULL || lane + 32 * j < a.E) ? bias[lane + 32 * j] : 0.f;
+    b[j] = NV <= HOISTED && bias && (FULL || lane + 32 * j < a.E) ? clean_bias(bias[lane + 32 * j]) : 0.f;
   const int64_t t0 = ((int64_t)blockIdx.x * ROUTER_WARPS + warp) * batch;
   if (t0 < a.T) {
     const int n = (int)min((int64_t)batch, a.T - t0);

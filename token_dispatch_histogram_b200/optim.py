@@ -31,6 +31,9 @@ class EpAdamW:
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits = state_bits
         self.device = params[0].device
+        where = [p.data_ptr() for p in params if p.numel()]
+        if len(set(where)) != len(where):
+            raise ValueError("a parameter stands twice in the list")
         if state is None:
             state = self._fresh()
         self.steps, self.m, self.v = state["step"], list(state["m"]), list(state["v"])
