@@ -270,8 +270,14 @@ __device__ __forceinline__ void unpack8(uint4 p, float* v) {
   }
 }
 
-// 1 / (1 + e^-g); e^-g overflows to infinity for g below -88, where the result is 0
-__device__ __forceinline__ float sigmoid_fast(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// 1 / (1 + e^-g) by the hardware's 2^x and reciprocal (2^-22 and 2^-23 of themselves; the exponent |g| 2^-24): far
+// inside bf16.  e^-g overflows to infinity for g below -88, where the result is 0.
+__device__ __forceinline__ float sigmoid_fast(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504088896341f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 
 // A warp's way between "a lane has a row" (as tensor memory gives it) and "four
 // lanes have 64 bytes of a row" (as global memory wants it): 32 rows of 64 bytes
