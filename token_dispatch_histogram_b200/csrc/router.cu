@@ -329,7 +329,8 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
         if (x[j] == -INFINITY) key[j] = -INFINITY;
     }
   }
-  // NaN: not there (past E, or of a group left out)
+  // Logits that are there: not past E, nor of a group left out.  The others' keys are -inf.
+  uint32_t there = 0xffffffffu;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
     if (FULL || lane + 32 * j < a.E) row[lane + 32 * j] = key[j];
@@ -341,7 +342,10 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
     for (int j = 0; j < NV; ++j) {
       if (group_scores) key[j] = x[j]; 
       const uint32_t g = (uint32_t)(lane + 32 * j) * a.group_inv >> 21;
-      if (!(keep >> g & 1)) key[j] = NAN;
+      if (!(keep >> g & 1)) {
+        key[j] = -INFINITY;
+        there &= ~(1u << j);
+      }
     }
     if (group_scores) {
 #pragma unroll
@@ -352,7 +356,10 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
   if (!FULL) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (lane + 32 * j >= a.E) key[j] = NAN;
+      if (lane + 32 * j >= a.E) {
+        key[j] = -INFINITY;
+        there &= ~(1u << j);
+      }
   }
   float own = NAN;
 #pragma unroll
@@ -366,9 +373,12 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
     }
   }
   if (isnan(t)) t = -INFINITY;
-  uint32_t mine = 0;
+  // Which keys reach t, by the sign of a difference (infinities of one sign give NaN, whose sign is plus): a sum and a
+  // shift, where a comparison and a selection would both take the integer pipe, which is the one that is busy here.
+  uint32_t below = 0;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) mine |= key[j] >= t ? 1u << j : 0u;
+  for (int j = NV - 1; j >= 0; --j) below = __funnelshift_l(__float_as_uint(key[j] - t), below, 1);
+  uint32_t mine = ~below & there & (NV == 32 ? 0xffffffffu : (1u << NV) - 1);
   const int count = __popc(mine);
   int n = 0, at = 0;
   for (int i = 1;; ++i) {
@@ -389,14 +399,15 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
   const int have = min(n, a.K + 1);
   if (n <= 32 && have <= 31) {
     const float k0 = lane < n ? list->key[lane] : NAN;
-    int r0 = 0;
+    uint32_t greater = 0;  // a bit for each candidate; NaN behind them
     for (int i = 0; i < n; i += 4) {
       const float4 o = *reinterpret_cast<const float4*>(list->key + i);
-      r0 += o.x > k0;
-      r0 += o.y > k0;
-      r0 += o.z > k0;
-      r0 += o.w > k0;
+      greater = __funnelshift_l(__float_as_uint(k0 - o.x), greater, 1);
+      greater = __funnelshift_l(__float_as_uint(k0 - o.y), greater, 1);
+      greater = __funnelshift_l(__float_as_uint(k0 - o.z), greater, 1);
+      greater = __funnelshift_l(__float_as_uint(k0 - o.w), greater, 1);
     }
+    const int r0 = __popc(greater);
     const bool in = lane < n && r0 < have;
     if (__reduce_or_sync(0xffffffffu, in ? 1u << r0 : 0u) == (1u << have) - 1) {  // no two of them have one rank
       if (in) {
@@ -449,8 +460,15 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3
       bool special = false;
 #pragma unroll
       for (int j = 0; j < NV; ++j) x[j] = FULL || lane + 32 * j < a.E ? to_f32(row[lane + 32 * j]) : -INFINITY;
+      if (FULL) {  // an infinity or NaN times 0 is NaN
+        float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) special |= !(fabsf(x[j]) <= FLT_MAX) && (FULL || lane + 32 * j < a.E);
+        for (int j = 0; j < NV; ++j) sum = fmaf(x[j], 0.f, sum);
+        special = sum != 0.f;
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) special |= !(fabsf(x[j]) <= FLT_MAX) && lane + 32 * j < a.E;
+      }
       special = __any_sync(0xffffffffu, special);
       if (special) {
         bool bad = false;
