@@ -34,7 +34,8 @@ def ref_router(x, K, score, bias=None, n_group=1, topk_group=1, group_top=1, ren
 
 def ref_scores(x, score):
     if score == "sigmoid":
-        return np.array([1 / (1 + np.exp(-v)) if v > -700 else 0.0 for v in x])
+        with np.errstate(over="ignore"):
+            return 1 / (1 + np.exp(-x))
     m = x.max()
     if m == -np.inf:
         return np.zeros_like(x)
@@ -130,6 +131,12 @@ MANY = [  # more tokens than there are warps at work: several to a warp
     (4801, 33, 20, "softmax", 0.05, 1, 1, 1, True, 1.0),
     (4801, 32, 32, "sigmoid", None, 1, 1, 1, True, 1.0),
     (4801, 16, 16, "softmax", 0.1, 1, 1, 1, True, 1.0),
+    (4802, 128, 8, "sigmoid", 0.1, 1, 1, 1, True, 1.0),
+    (4803, 128, 5, "softmax", None, 1, 1, 1, False, 1.0),
+    (4801, 100, 8, "softmax", 0.02, 1, 1, 1, True, 1.0),
+    (4801, 65, 1, "sigmoid", None, 1, 1, 1, False, 1.0),
+    (4801, 8, 8, "softmax", 0.1, 1, 1, 1, False, 1.0),
+    (4801, 3, 2, "sigmoid", 0.1, 1, 1, 1, True, 1.0),
 ]
 
 
@@ -180,6 +187,33 @@ def test_experts_closer_than_32_bit_scores_tell_apart(score, groups, bias):
     assert st == 0
     np.testing.assert_array_equal(ids, want_ids)
     assert np.all(np.abs(w - want) <= w_bound(x.astype(np.float64), want, ids, 1.0))
+
+
+@gpu
+@pytest.mark.parametrize("score,bias", [("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("E,K", [(64, 8), (100, 8), (128, 3), (200, 8)])
+def test_ties_and_unusual_logits_of_many_tokens(E, K, score, bias):
+    """Few different values, so that most choices are ties; masks, NaN and infinities among them."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    T = 4777
+    rng = np.random.default_rng(E + K)
+    x = rng.integers(-2, 3, (T, E)).astype(np.float32)
+    x[rng.random((T, E)) < 0.2] = -np.inf
+    x[5] = -np.inf
+    b = np.zeros(E, np.float32) if bias else None
+    kw = dict(score=score)
+    ids, w, st = call(torch.from_numpy(x).cuda(), K, bias=b, **kw)
+    b64 = None if b is None else b.astype(np.float64)
+    want_ids, want = ref_router(x.astype(np.float64), K, bias=b64, **kw)
+    assert st == 0
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(x.astype(np.float64), want, ids, 1.0))
+    x[7, 3], x[9, 1] = np.nan, np.inf
+    ids, w, st = call(torch.from_numpy(x).cuda(), K, bias=b, **kw)
+    assert st == tdh.EP_DEV_BAD_LOGIT
+    y = np.nan_to_num(x, nan=-np.inf, posinf=np.finfo(np.float32).max, neginf=-np.inf)
+    np.testing.assert_array_equal(ids, ref_router(y.astype(np.float64), K, bias=b64, **kw)[0])
 
 
 @gpu
@@ -330,7 +364,8 @@ def check_backward(got, want, mag, x):
 @pytest.mark.parametrize("masked", [0.0, 0.3])
 @pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
 @pytest.mark.parametrize("T,E,K", [(1, 1, 1), (1, 256, 8), (65, 64, 6), (33, 17, 17), (9, 1024, 32), (200, 384, 8),
-                                   (21, 100, 5), (5003, 64, 6), (4801, 45, 12), (4801, 300, 20)])
+                                   (21, 100, 5), (5003, 64, 6), (4801, 45, 12), (4801, 300, 20), (4802, 128, 8), (4803, 99, 3),
+                                   (4801, 5, 5), (4803, 300, 4)])
 def test_backward_matches_the_jacobian(T, E, K, score, renorm, masked, dtype):
     import torch
     import token_dispatch_histogram_b200 as tdh
@@ -374,13 +409,13 @@ def test_backward_matches_differences_of_the_forward(score, renorm):
 
 
 @gpu
-@pytest.mark.parametrize("T", [4, 4904])
-def test_backward_of_repeated_and_bad_ids(T):
+@pytest.mark.parametrize("T,E", [(4, 12), (4904, 12), (4904, 120), (4904, 130)])
+def test_backward_of_repeated_and_bad_ids(T, E):
     import torch
     import token_dispatch_histogram_b200 as tdh
-    E, K = 12, 5
+    K = 5
     x = logits_of(T, E, torch.float32, 8)
-    ids = np.array([[3, 3, 3, 1, 0], [2, 5, 2, 5, 2], [0, 12, -1, 4, 7], [-1, -1, 99, -5, 1 << 30]], np.int32)
+    ids = np.array([[3, 3, 3, 1, 0], [2, 5, 2, 5, 2], [0, E, -1, 4, 7], [-1, -1, 999, -5, 1 << 30]], np.int32)
     ids = np.tile(ids, (T // 4, 1))
     dw = torch.randn((T, K), generator=torch.Generator().manual_seed(1))
     for score in ("softmax", "sigmoid"):

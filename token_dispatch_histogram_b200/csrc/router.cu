@@ -26,6 +26,7 @@
 namespace ep {
 
 constexpr int ROUTER_WARPS = 8;
+constexpr int SMALL_E = 128;  // experts up to which eight lanes hold a token's logits
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -430,6 +431,76 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
   return true;
 }
 
+// Four consecutive elements as fp32, and back.
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 q = *reinterpret_cast<const float4*>(p);
+  v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+}
+template <typename V>
+__device__ __forceinline__ void load4(const V* p, float* v) {
+  const uint2 q = *reinterpret_cast<const uint2*>(p);
+  const V* h = reinterpret_cast<const V*>(&q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = to_f32(h[i]);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <typename V>
+__device__ __forceinline__ void store4(V* p, const float* v) {
+  uint2 q;
+  V* h = reinterpret_cast<V*>(&q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = from_f32<V>(v[i]);
+  *reinterpret_cast<uint2*>(p) = q;
+}
+
+// The end of a batch of tokens, `width` lanes to a token: lane k has its k-th
+// expert id and, if `next`, that one's key and its successor's key and expert.
+// Neighbours whose difference is within what both keys are off send their token to
+// select_exact; then the weights.  m, z: the softmax of the lane's token.
+template <typename V>
+__device__ __forceinline__ void finish_tokens(const RouterArgs& a, const V* __restrict__ logits,
+                                              const float* __restrict__ bias, int64_t t0, int width, bool live, int id,
+                                              bool next, float key0, float key1, int e1, float m, float z,
+                                              double* exact_keys, int32_t* __restrict__ ids, float* __restrict__ w) {
+  const int lane = threadIdx.x & 31, of = lane / width, k = lane % width;
+  const V* row = logits + (t0 + of) * a.ld;
+  if (bias) {
+    bool tight = false;
+    // a score of 1 bounds every error: only where that is not enough the scores themselves are looked at
+    if (next && key1 != -INFINITY &&
+        key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1)) {
+      const float b0 = bias[id], b1 = bias[e1];
+      tight = key0 - key1 <= key_error(a.sigmoid, key0 - b0, key0) + key_error(a.sigmoid, key1 - b1, key1);
+      if (tight && b0 == b1) tight = to_f32(row[id]) != to_f32(row[e1]);  // equal in truth: in order as it is
+    }
+    uint32_t again = __ballot_sync(0xffffffffu, tight);
+    while (again) {
+      const int i = (__ffs(again) - 1) / width;
+      const int e = select_exact(a, logits + (t0 + i) * a.ld, bias, exact_keys);
+      const int back = __shfl_sync(0xffffffffu, e, k);
+      if (of == i && live) id = back;
+      again &= ~((width == 32 ? 0xffffffffu : (1u << width) - 1) << (i * width));
+      __syncwarp();
+    }
+  }
+  bool ignore = false;
+  const float x = live ? clean_logit(to_f32(row[id]), ignore) : -INFINITY;
+  float v;
+  if (a.renorm)
+    v = chosen_ratio(x, a.sigmoid, width);
+  else if (a.sigmoid)
+    v = sigmoid_f32(x);
+  else
+    v = m == -INFINITY ? 0.f : exp_near(x - m) / z;
+  if (live) {
+    const int64_t to = (t0 + of) * a.K + k;
+    ids[to] = id;
+    w[to] = a.scale * v;
+  }
+}
+
 // A warp takes 32 / width tokens at a time: one after the other as far as the
 // choice goes, then together, width lanes a token (the next power of two from K,
 // at least 8), for what concerns the K chosen ones only.  A warp to a token the
@@ -493,70 +564,118 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32, NV <= 12 ? 4 : NV <= 16 ? 3
     }
     const int at = of * (a.K + 1) + k;
     const bool live = of < n && k < a.K;
-    const V* row = logits + (t0 + of) * a.ld;
-    int id = live ? list->sorted_e[at] : 0;
-    if (bias) {
-      // Neighbours whose difference is within what both are off.  (The (K + 1)-th is there unless there are only K.)
-      bool tight = false;
-      if (live && !(exact >> of & 1) && (k + 1 < a.K || a.more)) {
-        const float key0 = list->sorted_key[at], key1 = list->sorted_key[at + 1];
-        // a score of 1 bounds every error: only where that is not enough the scores themselves are looked at
-        if (key1 != -INFINITY && key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1)) {
-          const int e1 = list->sorted_e[at + 1];
-          const float b0 = bias[id], b1 = bias[e1];
-          tight = key0 - key1 <= key_error(a.sigmoid, key0 - b0, key0) + key_error(a.sigmoid, key1 - b1, key1);
-          if (tight && b0 == b1) tight = to_f32(row[id]) != to_f32(row[e1]);  // equal in truth: in order as it is
-        }
-      }
-      uint32_t again = __ballot_sync(0xffffffffu, tight);
-      while (again) {
-        const int i = (__ffs(again) - 1) / width;
-        const int e = select_exact(a, logits + (t0 + i) * a.ld, bias, mine);
-        const int back = __shfl_sync(0xffffffffu, e, k);
-        if (of == i && live) id = back;
-        again &= ~((width == 32 ? 0xffffffffu : (1u << width) - 1) << (i * width));
-        __syncwarp();
-      }
-    }
-    bool ignore = false;
-    const float xs = live ? clean_logit(to_f32(row[id]), ignore) : -INFINITY;
-    float v;
-    if (a.renorm)
-      v = chosen_ratio(xs, a.sigmoid, width);
-    else if (a.sigmoid)
-      v = sigmoid_f32(xs);
-    else
-      v = m == -INFINITY ? 0.f : exp_near(xs - m) / z;
-    if (live) {
-      const int64_t to = (t0 + of) * a.K + k;
-      ids[to] = id;
-      w[to] = a.scale * v;
-    }
+    // the (K + 1)-th is there unless there are only K
+    const bool next = live && !(exact >> of & 1) && (k + 1 < a.K || a.more);
+    finish_tokens(a, logits, bias, t0, width, live, live ? list->sorted_e[at] : 0, next,
+                  next ? list->sorted_key[at] : 0.f, next ? list->sorted_key[at + 1] : 0.f,
+                  next ? list->sorted_e[at + 1] : 0, m, z, mine, ids, w);
   }
 }
 
-// Four consecutive elements as fp32, and back.
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 q = *reinterpret_cast<const float4*>(p);
-  v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-}
-template <typename V>
-__device__ __forceinline__ void load4(const V* p, float* v) {
-  const uint2 q = *reinterpret_cast<const uint2*>(p);
-  const V* h = reinterpret_cast<const V*>(&q);
+// Many tokens over few experts (up to 8 * NE = 128, no groups, K up to 8): eight
+// lanes to a token, four tokens at once.  Each round takes the largest key over the
+// eight lanes, the lowest index where several have it, and strikes it out: what a
+// round costs is shared by four tokens, where a warp to a token spends it on one.
+// (262,144 tokens over 64 experts, softmax, K = 6: 58 us against 120; over 128
+// experts, K = 8: 99 against 118.)  Lane l has the elements 32 i + 4 l + j.
+template <typename V, int NE, bool VEC>
+__global__ void __launch_bounds__(ROUTER_WARPS * 32)
+    k_router_small(const V* __restrict__ logits, const float* __restrict__ bias, RouterArgs a,
+                   int32_t* __restrict__ ids, float* __restrict__ w, int32_t* dev_status) {
+  extern __shared__ double s_key[];  // [warps][E], of select_exact
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, of = lane >> 3, l = lane & 7;
+  wait_for_predecessor();
+  const int64_t t0 = ((int64_t)blockIdx.x * ROUTER_WARPS + warp) * 4;
+  if (t0 >= a.T) return;
+  const int n = (int)min((int64_t)4, a.T - t0);
+  const V* row = logits + (t0 + min(of, n - 1)) * a.ld;  // lanes without a token repeat the last one's
+  float x[NE], key[NE];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = to_f32(h[i]);
-}
-__device__ __forceinline__ void store4(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-template <typename V>
-__device__ __forceinline__ void store4(V* p, const float* v) {
-  uint2 q;
-  V* h = reinterpret_cast<V*>(&q);
+  for (int i = 0; i < NE / 4; ++i) {
+    const int e = 32 * i + 4 * l;
+    if (VEC) {
+      if (e < a.E) {
+        load4(row + e, x + 4 * i);
+      } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = from_f32<V>(v[i]);
-  *reinterpret_cast<uint2*>(p) = q;
+        for (int j = 0; j < 4; ++j) x[4 * i + j] = -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[4 * i + j] = e + j < a.E ? to_f32(row[e + j]) : -INFINITY;
+    }
+  }
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) bad |= !(x[i] <= FLT_MAX);
+  if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) x[i] = clean_logit(x[i], bad);
+    if (lane == 0) flag(dev_status, EP_DEV_BAD_LOGIT);
+  }
+  float m = -INFINITY, z = 0.f;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) key[i] = x[i];
+  if (!a.sigmoid && (bias || !a.renorm)) {  // softmax over the row
+#pragma unroll
+    for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+    for (int d = 4; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float m0 = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const float p = ex2_approx((x[i] - m0) * LOG2E);
+      z += p;
+      if (bias) key[i] = p;
+    }
+#pragma unroll
+    for (int d = 4; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+  }
+  if (bias) {
+    const float iz = z > 0.f ? rcp_approx(z) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = 32 * (i / 4) + 4 * l + i % 4;
+      key[i] = a.sigmoid ? rcp_approx(1.f + ex2_approx(x[i] * -LOG2E)) : key[i] * iz;
+      key[i] += e < a.E ? clean_bias(bias[e]) : 0.f;
+      if (x[i] == -INFINITY) key[i] = -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    if (32 * (i / 4) + 4 * l + i % 4 >= a.E) key[i] = NAN;  // not there
+  // lane k of a token keeps its k-th expert; the (K + 1)-th, for the one before it, every lane does
+  const int rounds = a.K + (bias && a.more ? 1 : 0);
+  float mine = 0.f, last = 0.f;
+  int id = 0, last_e = 0;
+  for (int r = 0; r < rounds; ++r) {
+    float g = NAN;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) g = fmaxf(g, key[i]);
+#pragma unroll
+    for (int d = 4; d; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
+    int at = NE;
+#pragma unroll
+    for (int i = NE - 1; i >= 0; --i) at = key[i] == g ? i : at;
+    const int e = at < NE ? 32 * (at >> 2) + 4 * l + (at & 3) : INT_MAX;
+    int first = e;
+#pragma unroll
+    for (int d = 4; d; d >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
+    if (first != e) at = NE;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) key[i] = i == at ? NAN : key[i];
+    if (l == r) {
+      mine = g;
+      id = first;
+    }
+    last = g;
+    last_e = first;
+  }
+  const bool live = of < n && l < a.K;
+  const float after = __shfl_down_sync(0xffffffffu, mine, 1);
+  const int after_e = __shfl_down_sync(0xffffffffu, id, 1);
+  finish_tokens(a, logits, bias, t0, 8, live, live ? id : 0, live && (l + 1 < a.K || a.more), mine,
+                l + 1 < a.K ? after : last, l + 1 < a.K ? after_e : last_e, m, z, s_key + (size_t)warp * a.E, ids, w);
 }
 
 // The gradient of the weights.  With r_k = s_k / sum_j s_j:
@@ -697,6 +816,126 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32)
   if (bits && lane == 0) flag(dev_status, bits);
 }
 
+// The same for many tokens over few experts: eight lanes to a token as in
+// k_router_small, four tokens at once.  (262,144 tokens over 64 experts, softmax over
+// all, K = 6, bf16: 33 us against 82.)
+template <typename V, int NE, bool VEC>
+__global__ void __launch_bounds__(ROUTER_WARPS * 32)
+    k_router_backward_small(const float* __restrict__ dw, const V* __restrict__ logits,
+                            const int32_t* __restrict__ ids, RouterArgs a, int64_t ld_out, V* __restrict__ dlogits,
+                            int32_t* dev_status) {
+  __shared__ __align__(16) float s_row[ROUTER_WARPS * 4 * 8 * NE];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, of = lane >> 3, l = lane & 7;
+  float* out = s_row + (warp * 4 + of) * 8 * NE;  // this token's row
+#pragma unroll
+  for (int i = 0; i < NE / 4; ++i) *reinterpret_cast<float4*>(out + 32 * i + 4 * l) = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncwarp();
+  wait_for_predecessor();
+  const int64_t t0 = ((int64_t)blockIdx.x * ROUTER_WARPS + warp) * 4;
+  if (t0 >= a.T) return;
+  const int n = (int)min((int64_t)4, a.T - t0);
+  const int64_t t = t0 + min(of, n - 1);
+  const V* row = logits + t * a.ld;
+  const bool dense = !a.sigmoid && !a.renorm, live = of < n && l < a.K;
+  uint32_t bits = 0;
+  bool bad = false;
+  int id = -1;
+  float x = -INFINITY, d = 0.f;
+  if (live) {
+    id = ids[t * a.K + l];
+    if (id < 0 || id >= a.E) {
+      bits |= EP_DEV_BAD_EXPERT_ID;
+      id = -1;
+    } else {
+      d = dw[t * a.K + l];
+      x = clean_logit(to_f32(row[id]), bad);
+    }
+  }
+  float p[NE], v = 0.f, inner = 0.f;  // v: this lane's term of dlogits[id], without the scale
+  if (dense) {
+    float m = -INFINITY, z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NE / 4; ++i) {
+      const int e = 32 * i + 4 * l;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[4 * i + j] = -INFINITY;
+      if (VEC) {
+        if (e < a.E) load4(row + e, p + 4 * i);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (e + j < a.E) p[4 * i + j] = to_f32(row[e + j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[4 * i + j] = clean_logit(p[4 * i + j], bad);
+        m = fmaxf(m, p[4 * i + j]);
+      }
+    }
+#pragma unroll
+    for (int s = 4; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    const float m0 = m == -INFINITY ? 0.f : m;  // a row of -inf has scores of 0
+#pragma unroll
+    for (int i = 0; i < NE; ++i) z += p[i] = exp_near(p[i] - m0);
+#pragma unroll
+    for (int s = 4; s; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
+    const float iz = z > 0.f ? 1.f / z : 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) p[i] *= iz;
+    v = d * (exp_near(x - m0) * iz);
+    inner = v;
+#pragma unroll
+    for (int s = 4; s; s >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, s);
+    inner *= a.scale;
+  } else if (a.renorm) {
+    const float r = chosen_ratio(x, a.sigmoid, 8);
+    float i = d * r;
+#pragma unroll
+    for (int s = 4; s; s >>= 1) i += __shfl_xor_sync(0xffffffffu, i, s);
+    v = r * (d - i);
+    if (a.sigmoid) v *= sigmoid_f32(-x);
+  } else {
+    v = d * sigmoid_f32(x) * sigmoid_f32(-x);
+  }
+  // of lanes with the same expert of the same token, the first lays down the sum of all, in order
+  float mine = a.scale * v;
+  uint32_t same = 0;
+  for (int j = 0; j < a.K; ++j) same |= __shfl_sync(0xffffffffu, id, of * 8 + j) == id ? 1u << j : 0u;
+  if (__any_sync(0xffffffffu, id >= 0 && (same & (same - 1)))) {
+    float sum = 0.f;
+    for (int j = 0; j < a.K; ++j) {
+      const float o = __shfl_sync(0xffffffffu, mine, of * 8 + j);
+      if (same >> j & 1) sum += o;
+    }
+    mine = sum;
+  }
+  if (id >= 0 && (same & ((1u << l) - 1)) == 0) out[id] = mine;
+  __syncwarp();
+  V* to = dlogits + t * ld_out;
+#pragma unroll
+  for (int i = 0; i < NE / 4; ++i) {
+    const int e = 32 * i + 4 * l;
+    if (of < n && e < a.E) {
+      const float4 q = *reinterpret_cast<const float4*>(out + e);
+      float o[4] = {q.x, q.y, q.z, q.w};
+      if (dense) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] -= inner * p[4 * i + j];
+      }
+      if (VEC) {
+        store4(to + e, o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (e + j < a.E) to[e + j] = from_f32<V>(o[j]);
+      }
+    }
+  }
+  if (bad) bits |= EP_DEV_BAD_LOGIT;
+  bits = __reduce_or_sync(0xffffffffu, bits);
+  if (bits && lane == 0) flag(dev_status, bits);
+}
+
 static bool valid_router(int dtype, int64_t T, int E, int64_t ld, int K, int score, float scale) {
   if (!valid_tke(T, K, E) || ld < E) return false;
   if (dtype != EP_DTYPE_F32 && dtype != EP_DTYPE_BF16 && dtype != EP_DTYPE_F16) return false;
@@ -725,6 +964,19 @@ static int launch_router(const void* logits, const float* bias, const RouterArgs
   return EP_OK;
 }
 
+template <typename V, int NE>
+static int launch_small(const void* logits, const float* bias, const RouterArgs& a, int32_t* ids, float* w,
+                        int32_t* dev_status, cudaStream_t stream) {
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && aligned_to(logits, 4 * sizeof(V));
+  const void* fn = vec ? (const void*)k_router_small<V, NE, true> : (const void*)k_router_small<V, NE, false>;
+  void* args[] = {&logits, &bias, (void*)&a, &ids, &w, &dev_status};
+  if (launch_pdl(fn, dim3((unsigned)((a.T + 4 * ROUTER_WARPS - 1) / (4 * ROUTER_WARPS))), dim3(ROUTER_WARPS * 32), args,
+                 (size_t)ROUTER_WARPS * a.E * sizeof(double), stream) != cudaSuccess)
+    return EP_ERR_CUDA;
+  count_launch();
+  return EP_OK;
+}
+
 template <typename V>
 static int run_router(const void* logits, const float* bias, RouterArgs a, int32_t* ids, float* w, int32_t* dev_status,
                       cudaStream_t stream) {
@@ -734,6 +986,10 @@ static int run_router(const void* logits, const float* bias, RouterArgs a, int32
   a.more = (a.n_group == 1 ? a.E : a.topk_group * len) > a.K;
   a.width = router_width(a);
   a.group_inv = ((1u << 21) + len - 1) / len;
+  if (a.width == 8 && a.n_group == 1 && a.E <= SMALL_E) {
+    if (a.E <= 64) return launch_small<V, 8>(logits, bias, a, ids, w, dev_status, stream);
+    return launch_small<V, 16>(logits, bias, a, ids, w, dev_status, stream);
+  }
   // logits a lane: the next of these up from E / 32
 #define EP_ROUTER(nv)                                                                       \
   if (a.E == 32 * nv) return launch_router<V, nv, true>(logits, bias, a, ids, w, dev_status, stream); \
@@ -769,6 +1025,18 @@ static int run_router_backward(const float* dw, const void* logits, const int32_
   a.width = router_width(a);
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && ld_out % 4 == 0 && aligned_to(logits, 4 * sizeof(V)) &&
                    aligned_to(dlogits, 4 * sizeof(V));
+  if (a.width == 8 && a.E <= SMALL_E) {
+    const void* fn = a.E <= 64 ? vec ? (const void*)k_router_backward_small<V, 8, true>
+                                     : (const void*)k_router_backward_small<V, 8, false>
+                               : vec ? (const void*)k_router_backward_small<V, 16, true>
+                                     : (const void*)k_router_backward_small<V, 16, false>;
+    void* args[] = {&dw, &logits, &ids, (void*)&a, &ld_out, &dlogits, &dev_status};
+    if (launch_pdl(fn, dim3((unsigned)((a.T + 4 * ROUTER_WARPS - 1) / (4 * ROUTER_WARPS))), dim3(ROUTER_WARPS * 32),
+                   args, 0, stream) != cudaSuccess)
+      return EP_ERR_CUDA;
+    count_launch();
+    return EP_OK;
+  }
 #define EP_BACKWARD(nc)                                                                                            \
   if (a.E <= 128 * nc)                                                                                             \
   return vec ? launch_backward<V, nc, true>(dw, logits, ids, a, ld_out, dlogits, dev_status, stream)               \
