@@ -392,8 +392,8 @@ EP_API int ep_dispatch(const uint16_t* x, int64_t T, int K, int64_t H, const int
                 int64_t buf_rows, int32_t* dev_status, cudaStream_t stream);
 
 /*
- * Stand-in for the expert computation (the grouped GEMM is outside this
- * library's path), for tests and examples: y[i] = bf16_rn(float(buf[i]) *
+ * Stand-in for the expert computation (ep_expert_up and ep_expert_gemm are the
+ * real one), for tests of the row movers alone: y[i] = bf16_rn(float(buf[i]) *
  * scale[e]) with e = topk_ids[src[i]], fp32 multiply.  y may alias buf.
  */
 EP_API int ep_expert_scale(const uint16_t* buf, int64_t rows, int64_t H, const int32_t* src, const int32_t* topk_ids,
