@@ -7,18 +7,27 @@
 //   ep_expert_wgrad        g_s = a_s^T b_s, fp32
 //
 // One persistent kernel per form, one CTA per SM, two CTAs (a cluster) on one
-// tile of 256 x 256: each holds half of both operands and half of the result's
-// rows.  Alone, a CTA with a 128 x 256 tile would read 12 KB of operands per
-// product of 128 cycles and write as much for the next, more than the 128 bytes
-// per cycle its shared memory takes; a pair shares the second operand and needs
-// 8 KB each.  A pair walks output tiles in a fixed order; the slots' row counts
-// are on the device, so every CTA first scans them into shared memory (tiles
-// before each slot) and finds a tile's slot there by bisection (warp 2, some tiles
-// ahead): no launch depends on a count the host would have to read.  In each CTA
+// tile: 256 rows by 512 columns in two accumulators (one of 256 in the weight
+// gradient), of which each CTA holds half of the rows and half of each operand.
+// Alone, a CTA with a 128 x 256 tile would read 12 KB of operands per product of
+// 128 cycles and write as much for the next, more than the 128 bytes per cycle its
+// shared memory takes; a pair shares the second operand and needs 8 KB each.  Two
+// accumulators share the rows' operand too, so a quarter less comes from L2.  A
+// pair walks output tiles in a fixed order; the slots' row counts are on the
+// device, so every CTA first scans them into shared memory (tiles before each
+// slot) and finds a tile's slot there by bisection (warp 2, some tiles ahead): no
+// launch depends on a count the host would have to read.  In each CTA a thread of
 // warp 0 brings operand tiles of 64 along the contraction into a ring in shared
-// memory (TMA, 128-byte swizzle); the leader's warp 1 issues the tensor-core
-// products into one of two accumulators in tensor memory; warps 4-11 take the
-// other accumulator through the epilogue to global memory meanwhile.
+// memory (TMA, 128-byte swizzle); one of the leader's warp 1 issues the tensor-core
+// products into the accumulators in tensor memory; warps 4-11 take a finished
+// accumulator into registers, give it back, and bring it through the epilogue to
+// global memory while the next tile's products run.
+//
+// Measured (B200, after a pause): second projection of 32,768 rows in 13 slots, H
+// 7168, I 2048, 676 us = 1424 TFLOP/s (the library's product of one such matrix 627);
+// first projection of 196,608 rows in 64 slots, H 2048, I 1024, its products kept,
+// 1240 us = 1330; weight gradient of the same 705 us = 1170; backward of the activation
+// at the first size 800 us = 1203.  In a loop the power cap takes 10 % off all of them.
 //
 // A tile's rows are its slot's rows from a multiple of 256 on; rows behind the
 // slot's end belong to the next slot and only make accumulator rows that are
@@ -113,9 +122,10 @@ struct Slot {
   int len, w;
 };
 
+// The tables are read past L1: the kernel may start while the one that writes them ends.
 template <Form F>
 __device__ __forceinline__ Slot load_slot(const ExpertArgs& a, int s, int32_t* bits) {
-  const int id = a.slots ? __ldg(a.slots + s) : s;
+  const int id = a.slots ? __ldcg(a.slots + s) : s;
   Slot r{0, -1, id};
   if (id < 0) return r;
   if (id >= a.n_w + a.n_rep || (id >= a.n_w && F != WGRAD && !a.rep)) {
@@ -123,13 +133,13 @@ __device__ __forceinline__ Slot load_slot(const ExpertArgs& a, int s, int32_t* b
     return r;
   }
   if (F != WGRAD && id >= a.n_w) {
-    r.w = __ldg(a.rep + (id - a.n_w));
+    r.w = __ldcg(a.rep + (id - a.n_w));
     if (r.w < 0 || r.w >= a.n_w) {
       *bits |= EP_DEV_BAD_EXPERT_ID;
       return r;
     }
   }
-  const int b = __ldg(a.cu + s), e = __ldg(a.cu + s + 1);
+  const int b = __ldcg(a.cu + s), e = __ldcg(a.cu + s + 1);
   if (b < 0 || e < b || e > a.rows) {
     *bits |= EP_DEV_BAD_ROW;
     return r;
