@@ -161,15 +161,14 @@ def _dtype(t, *dts):
 
 
 # The calls around the path (router, experts' products, optimizer) are made with
-# few tokens too, where the host's time counts: addresses go as plain integers, and
-# a device or stream object is only made where the caller's differ.
+# few tokens too, where the host's time counts: addresses go as plain integers,
+# devices are compared by their index, and a device or stream object is only made
+# where the caller's differ.  _launch refuses what is not on one GPU.
 
 def _at(t):
-    """Address of a contiguous CUDA tensor (None: none)."""
+    """Address of a contiguous tensor (None: none)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return t.data_ptr()
@@ -177,8 +176,8 @@ def _at(t):
 
 def _rows(t):
     """Address and row stride of a 2-d tensor whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
+    if t.is_contiguous() and t.dim() == 2:
+        return t.data_ptr(), t.shape[1]
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("expected a 2-d tensor with contiguous rows")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
@@ -189,22 +188,28 @@ def _shape(what, t, *shape):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
 
 
-def _launch(name, args, stream, *tensors):
+def _launch(name, args, stream, first, *others):
     """Call `name` with args and a stream (the current one of the tensors' device
     unless given) while the tensors' device is current; they must share one."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"tensors on {dev} and a stream on {stream.device}")
-    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    f = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        _check(name, f(*args, raw))
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("expected a CUDA tensor")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
     else:
-        with torch.cuda.device(dev):
-            _check(name, f(*args, raw))
+        if stream.device.index != index:
+            raise ValueError(f"tensors on {first.device} and a stream on {stream.device}")
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        code = getattr(_lib, name)(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            code = getattr(_lib, name)(*args, raw)
+    if code != EP_OK:
+        raise EpError(name, code)
 
 
 def version():
@@ -577,17 +582,24 @@ _SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
 
 
 def _router_args(logits, topk_ids, w, score):
-    _dtype(logits, *_LOGIT_DTYPES)
-    _dtype(topk_ids, torch.int32)
-    _dtype(w, torch.float32)
-    if score not in _SCORES:
+    dt = _LOGIT_DTYPES.get(logits.dtype)
+    if dt is None:
+        _dtype(logits, *_LOGIT_DTYPES)
+    if topk_ids.dtype is not torch.int32:
+        _dtype(topk_ids, torch.int32)
+    if w.dtype is not torch.float32:
+        _dtype(w, torch.float32)
+    sc = _SCORES.get(score)
+    if sc is None:
         raise ValueError(f"score {score!r}, expected one of {sorted(_SCORES)}")
     x, ld = _rows(logits)
     T, E = logits.shape
-    K = topk_ids.shape[1]
-    _shape("topk_ids", topk_ids, T, K)
-    _shape("gate weights", w, T, K)
-    return x, T, E, ld, K, _LOGIT_DTYPES[logits.dtype], _SCORES[score]
+    shape = topk_ids.shape
+    if len(shape) != 2 or shape[0] != T:
+        _shape("topk_ids", topk_ids, T, "K")
+    if w.shape != shape:
+        _shape("gate weights", w, *shape)
+    return x, T, E, ld, shape[1], dt, sc
 
 
 def ep_router(logits, topk_ids, w, score="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renorm=True,
@@ -743,6 +755,8 @@ def adamw_table(params, grads, m, v, m_scale=None, v_scale=None, copies=None):
             _dtype(t, dt)
             if t.numel() != count:
                 raise ValueError(f"{field} of tensor {i}: {t.numel()} elements, expected {count}")
+            if not t.is_cuda:
+                raise ValueError("expected a CUDA tensor")
             if t.device != params[0].device:
                 raise ValueError(f"tensors on {params[0].device} and {t.device}")
             setattr(table[i], field, _at(t) or None)
