@@ -298,6 +298,28 @@ def test_a_tensor_of_many_blocks_is_covered_once():
 
 
 @gpu
+def test_offsets_past_32_bits():
+    import torch
+    from token_dispatch_histogram_b200.optim import EpAdamW
+    n, tail = (1 << 31) + 256 * 3 + 50, 5000
+    p = torch.zeros(n, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    p[-tail:], g[-tail:] = torch.randn(tail, device="cuda"), torch.randn(tail, device="cuda").bfloat16()
+    was, grad = p[-tail:].cpu().numpy(), g[-tail:].float().cpu().numpy()
+    opt = EpAdamW([p], [g], lr=1e-2, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, state_bits=8)
+    opt.step()
+    c = constants(1, 1e-2, 0.9, 0.95, 1e-8, 0.1)
+    w, m, v, root = ref_update(was, grad, np.zeros(tail, F), np.zeros(tail, F), c)
+    np.testing.assert_array_equal(p[-tail:].cpu().numpy(), w)
+    assert torch.all(p[:-tail] == 0) and torch.all(opt.m[0].view(torch.uint8)[:-tail] == 0)
+    # whole blocks of the tail, which starts inside one
+    skip = (-(n - tail)) % BLOCK
+    codes, scales = ref_encode(m[skip:], False)
+    assert torch.equal(opt.m[0][-tail + skip:].view(torch.uint8).cpu(), codes)
+    np.testing.assert_array_equal(opt.m_scale[0][-scales.size:].cpu().numpy(), scales)
+
+
+@gpu
 def test_learning_rate_and_scale_on_the_device_and_a_replayed_graph():
     import torch
     case, other = Case([1000, 300], 8, copy=True), Case([1000, 300], 8, copy=True)

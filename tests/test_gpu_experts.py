@@ -430,6 +430,55 @@ def test_weight_gradients_of_many_slots_of_unlike_length(n, M, N):
 
 
 @gpu
+def test_offsets_past_32_bits():
+    """Rows whose elements lie past 2^31: the last slot's results, in every form."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    N, K, E = 8192, 64, 3
+    P = (1 << 31) // N + 700
+    cu = torch.tensor([0, P - 500, P - 130, P], dtype=torch.int32, device="cuda")
+    x = torch.zeros((P, K), dtype=torch.bfloat16, device="cuda")
+    x[P - 600:] = values((600, K), 1, True)
+    w = values((E, N, K), 2, True)
+    last = [slice(P - 500, P - 130), slice(P - 130, P)]
+
+    def exact(got, a, b, e):
+        want = a.double() @ b.double()
+        assert torch.equal(got, want.to(torch.bfloat16)), e
+
+    y = torch.empty((P, N), dtype=torch.bfloat16, device="cuda")
+    tdh.ep_expert_gemm(x, w, cu, y)
+    for e, r in enumerate(last, 1):
+        exact(y[r], x[r], w[e].T, e)
+    assert torch.all(y[:1000] == 0)
+    back = torch.empty((P, K), dtype=torch.bfloat16, device="cuda")
+    tdh.ep_expert_gemm(y, values((E, N, K), 3, True), cu, back, transpose_w=True)
+    w3 = values((E, N, K), 3, True)
+    for e, r in enumerate(last, 1):
+        want, mag = y[r].double() @ w3[e].double(), y[r].double().abs() @ w3[e].double().abs()
+        check(back[r], want, rounded(sum_bound(N, mag), want, back.dtype))
+    h = torch.empty((P, N // 2), dtype=torch.bfloat16, device="cuda")
+    gu = torch.empty((P, N), dtype=torch.bfloat16, device="cuda")
+    tdh.ep_expert_up(x, w, cu, h, gu)
+    assert torch.equal(gu[P - 500:], y[P - 500:])
+    dgu = y.zero_()
+    w2 = values((E, K, N // 2), 4, True)
+    tdh.ep_expert_up_backward(x, w2, gu, cu, dgu, h)
+    for e, r in enumerate(last, 1):
+        dh = x[r].double() @ w2[e].double()
+        g, u = gu[r].double().chunk(2, 1)
+        act = silu(g) * u
+        check(h[r], act, rounded(act.abs() * (g.abs() + 16) * 2.0 ** -21, act, h.dtype))
+        du = dh * silu(g)
+        check(dgu[r][:, N // 2:], du, rounded(du.abs() * (g.abs() + 16) * 2.0 ** -21, du, dgu.dtype))
+    g = torch.empty((E, N, K), device="cuda")
+    tdh.ep_expert_wgrad(gu, x, cu, g)
+    for e, r in enumerate(last, 1):
+        want, mag = gu[r].double().T @ x[r].double(), gu[r].double().abs().T @ x[r].double().abs()
+        check(g[e], want, rounded(sum_bound(512, mag), want, g.dtype))
+
+
+@gpu
 def test_two_streams_and_a_replayed_graph_give_the_same_bits():
     import torch
     import token_dispatch_histogram_b200 as tdh

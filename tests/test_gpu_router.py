@@ -250,6 +250,53 @@ def test_far_logits_keep_their_ratios(score, renorm):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("E", [64, 100, 256])
+def test_many_rows_of_a_wider_matrix(E, dtype):
+    """The forms for many tokens at any row stride and start, and the rows next to theirs left alone."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    T, K = 4801, 6
+    wide = logits_of(T, E + 67, getattr(torch, dtype), 9).cuda()
+    for off in (0, 1, 4):
+        x = wide[:, off:off + E]
+        ids = torch.full((T, K), -7, dtype=torch.int32, device="cuda")
+        w = torch.full((T, K), 77.0, device="cuda")
+        tdh.ep_router(x, ids, w, score="softmax", renorm=False)
+        want_ids, want = ref_router(x.double().cpu().numpy(), K, "softmax", renorm=False)
+        np.testing.assert_array_equal(ids.cpu().numpy(), want_ids)
+        assert np.all(np.abs(w.cpu().numpy() - want) <= w_bound(x.double().cpu().numpy(), want, want_ids, 1.0))
+        out = torch.full((T, E + 67), 5.0, dtype=wide.dtype, device="cuda")
+        dw = torch.randn((T, K), device="cuda")
+        tdh.ep_router_backward(dw, x, ids, out[:, off:off + E], score="softmax", renorm=False)
+        want, mag = ref_backward(dw.double().cpu().numpy(), x.double().cpu().numpy(), want_ids, "softmax", False, 1.0)
+        check_backward(out[:, off:off + E], want, mag, x)
+        assert torch.all(out[:, :off] == 5.0) and torch.all(out[:, off + E:] == 5.0)
+
+
+@gpu
+@pytest.mark.parametrize("E", [96, 384])
+def test_offsets_past_32_bits(E):
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    T, K = (1 << 31) // E + 5000, 4
+    x = torch.empty((T, E), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, T, 1 << 22):
+        x[i:i + (1 << 22)] = torch.randn((min(1 << 22, T - i), E), device="cuda", dtype=torch.bfloat16)
+    ids, w = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
+    tdh.ep_router(x, ids, w)
+    out = torch.empty_like(x)
+    tdh.ep_router_backward(w, x, ids, out)
+    for rows in (slice(0, 100), slice(T - 300, T)):
+        x64 = x[rows].double().cpu().numpy()
+        want_ids, want = ref_router(x64, K, "softmax")
+        np.testing.assert_array_equal(ids[rows].cpu().numpy(), want_ids)
+        assert np.all(np.abs(w[rows].cpu().numpy() - want) <= w_bound(x64, want, want_ids, 1.0))
+        want, mag = ref_backward(w[rows].double().cpu().numpy(), x64, want_ids, "softmax", True, 1.0)
+        check_backward(out[rows], want, mag, x[rows])
+
+
+@gpu
 def test_nan_and_infinite_logits_are_flagged_and_defined():
     import torch
     import token_dispatch_histogram_b200 as tdh
