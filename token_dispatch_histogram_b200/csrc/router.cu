@@ -311,18 +311,31 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
     for (int j = 0; j < NV; ++j) {
       const float p = ex2_approx((x[j] - m0) * LOG2E);
       sum += p;
-      if (scores) key[j] = p;
+      key[j] = p;
     }
     z = warp_sum(sum);
+    if (!scores) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] = x[j];
+    }
   }
   *top_logit = m;
   *total = z;
-  if (scores) {
-    const float iz = z > 0.f ? rcp_approx(z) : 0.f;
+  if (scores) {  // one loop to a step: a choice inside would be made for every element
+    if (a.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      key[j] = a.sigmoid ? rcp_approx(1.f + ex2_approx(x[j] * -LOG2E)) : key[j] * iz;
-      if (bias) key[j] += NV <= HOISTED ? b[j] : FULL || lane + 32 * j < a.E ? clean_bias(bias[lane + 32 * j]) : 0.f;
+      for (int j = 0; j < NV; ++j) key[j] = rcp_approx(1.f + ex2_approx(x[j] * -LOG2E));
+    } else {
+      const float iz = z > 0.f ? rcp_approx(z) : 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] *= iz;
+    }
+    if (NV <= HOISTED) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] += b[j];  // 0 without a bias
+    } else if (bias) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] += FULL || lane + 32 * j < a.E ? clean_bias(bias[lane + 32 * j]) : 0.f;
     }
     if (masked) {
 #pragma unroll
@@ -632,11 +645,17 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32)
     for (int d = 4; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
   }
   if (bias) {
-    const float iz = z > 0.f ? rcp_approx(z) : 0.f;
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) key[i] = rcp_approx(1.f + ex2_approx(x[i] * -LOG2E));
+    } else {
+      const float iz = z > 0.f ? rcp_approx(z) : 0.f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) key[i] *= iz;
+    }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const int e = 32 * (i / 4) + 4 * l + i % 4;
-      key[i] = a.sigmoid ? rcp_approx(1.f + ex2_approx(x[i] * -LOG2E)) : key[i] * iz;
       key[i] += e < a.E ? clean_bias(bias[e]) : 0.f;
       if (x[i] == -INFINITY) key[i] = -INFINITY;
     }
