@@ -217,6 +217,24 @@ def test_ties_and_unusual_logits_of_many_tokens(E, K, score, bias):
 
 
 @gpu
+@pytest.mark.parametrize("T", [200, 4801])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_whose_large_biases_cancel(score, T):
+    """Keys near 1000 and -999 whose sum is decided far below their own last place in 32 bits."""
+    import torch
+    E, K = 16, 2
+    rng = np.random.default_rng(3)
+    x = (rng.uniform(-1, 1, (T, 1)) + 2e-6 * rng.standard_normal((T, E))).astype(np.float32)
+    bias = np.array([1000, -999] + [-2000] * 6 + [0.5, 0.5] + [-5] * 6, np.float32)
+    kw = dict(score=score, n_group=2, topk_group=1, group_top=2)
+    ids, w, st = call(torch.from_numpy(x).cuda(), K, bias=bias, **kw)
+    want_ids, want = ref_router(x.astype(np.float64), K, bias=bias.astype(np.float64), **kw)
+    assert st == 0
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(x.astype(np.float64), want, ids, 1.0))
+
+
+@gpu
 @pytest.mark.parametrize("E,K", [(64, 8), (96, 32), (1024, 5)])
 @pytest.mark.parametrize("what", ["equal", "lowest", "two values", "signed zeros"])
 def test_ties_go_to_the_lower_index(E, K, what):

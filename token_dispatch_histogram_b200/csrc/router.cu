@@ -265,10 +265,14 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* ro
     second = fmaxf(fminf(first, f), fmaxf(second, o));
     first = fmaxf(first, f);
   }
-  float score = first;
-  if (a.group_top == 2 && second != -INFINITY) score += second;
-  // of two keys: twice the error of one, and the sum's rounding; s is at most 1
-  const float near = approximate ? 4.f * key_error(a.sigmoid, 1.f, 0.f) + 6e-7f * fabsf(score) : 0.f;
+  // off: what the score may be off, from its keys' errors (s is at most 1; the keys may be large and cancel) and the
+  // sum's rounding
+  float score = first, off = key_error(a.sigmoid, 1.f, first);
+  if (a.group_top == 2 && second != -INFINITY) {
+    score += second;
+    off += key_error(a.sigmoid, 1.f, second) + 1.2e-7f * fabsf(score);
+  }
+  const float near = off + warp_fmax(g < a.n_group ? off : 0.f);  // with any other group's
   int before = 0;
   uint32_t close = 0;
   for (int i = 0; i < a.n_group; ++i) {
