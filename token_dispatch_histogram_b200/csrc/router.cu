@@ -485,9 +485,12 @@ __device__ __forceinline__ void finish_tokens(const RouterArgs& a, const V* __re
   const V* row = logits + (t0 + of) * a.ld;
   if (bias) {
     bool tight = false;
-    // a score of 1 bounds every error: only where that is not enough the scores themselves are looked at
-    if (next && key1 != -INFINITY &&
-        key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1)) {
+    // A score of 1 bounds every error.  Between two chosen ones the errors of their own scores decide where that is not
+    // enough (one that overtakes several lies within them of the one before it); behind the last one stand experts whose
+    // keys are not at hand, so there any score has to be allowed for.
+    tight = next && key1 != -INFINITY &&
+            key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1);
+    if (tight && k + 1 < a.K) {
       const float b0 = bias[id], b1 = bias[e1];
       tight = key0 - key1 <= key_error(a.sigmoid, key0 - b0, key0) + key_error(a.sigmoid, key1 - b1, key1);
       if (tight && b0 == b1) tight = to_f32(row[id]) != to_f32(row[e1]);  // equal in truth: in order as it is
