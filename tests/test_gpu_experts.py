@@ -366,6 +366,35 @@ def test_an_id_at_two_slots_has_no_gradient_row(n):
 
 
 @gpu
+@pytest.mark.parametrize("n_slots", [40, 700])
+def test_weight_gradients_of_the_largest_ids(n_slots):
+    """1024 experts and as many replica rows as a call takes: ids up to 4094, some of them at two slots."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    E, cap, M, N = 1024, 3071, 8, 8
+    lens = [int(v) for v in np.random.default_rng(n_slots).integers(0, 5, n_slots)]
+    buf = Buffer(lens, replicas=False)
+    a, b = values((buf.P, M), 1, True), values((buf.P, N), 2, True)
+    # the highest ids, and those 3072 below them
+    high = E + cap - 1 - np.arange(n_slots - n_slots // 2)
+    order = np.concatenate([high[:n_slots // 2] - 3072, high]).astype(np.int32)
+    for twice in (False, True):
+        if twice:
+            order[3] = order[n_slots - 1]
+        home, rep, st = out((E, M, N), dtype=torch.float32), out((cap, M, N), dtype=torch.float32), status()
+        tdh.ep_expert_wgrad(a, b, buf.cu[:n_slots + 1], home, rep, slot_order=torch.from_numpy(order).cuda(),
+                            dev_status=st)
+        assert tdh.ep_status_read(st) == (tdh.EP_DEV_BAD_EXPERT_ID if twice else 0)
+        want = torch.full((E + cap, M, N), 7.0, dtype=torch.float64, device="cuda")
+        left_out = (3, n_slots - 1) if twice else ()
+        grads, _ = wgrad_want(buf, a, b)
+        for s in range(n_slots):
+            if s not in left_out:
+                want[order[s]] = grads[s]
+        assert torch.equal(torch.cat([home, rep]).double(), want)
+
+
+@gpu
 def test_no_rows_and_no_slots():
     import torch
     import token_dispatch_histogram_b200 as tdh

@@ -83,6 +83,7 @@ constexpr int TILES_AHEAD = 4;
 constexpr int SORTED_SLOTS = 512;
 constexpr int PART = 8;  // WGRAD: blocks of TK rows that the accumulator sums by itself
 constexpr int MAX_SLOTS = 2 * EP_MAX_EXPERTS + EP_MAX_RANKS - 1;  // E homes and E + R - 1 replicas
+constexpr int MAX_IDS = EP_MAX_EXPERTS + MAX_SLOTS;  // ids of slots lie below n_w + n_rep, and n_rep alone may be MAX_SLOTS
 constexpr int BAND = 8;  // tiles of a slot are walked in bands of 8 row blocks, so that the CTAs at work at a
                          // time share both operands in L2 (4 to 16 measured the same)
 
@@ -169,7 +170,7 @@ struct ExpertShared {
   int abort;
   int32_t warp_sums[32];
   uint16_t sorted[SORTED_SLOTS];  // WGRAD: the slots by descending rows
-  uint32_t seen[(MAX_SLOTS + 31) / 32], twice[(MAX_SLOTS + 31) / 32];  // WGRAD: ids, and those that stand twice
+  uint32_t seen[(MAX_IDS + 31) / 32], twice[(MAX_IDS + 31) / 32];  // WGRAD: ids, and those that stand twice
   int32_t before[MAX_SLOTS + 1];  // tiles before each slot
 };
 
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
     // Ranking each slot against all others is quick up to some hundred slots; longer tables stay as they are.
     const bool sorted = F == WGRAD && a.n_slots <= SORTED_SLOTS;
     if (F == WGRAD) {
-      for (int i = tid; i < (MAX_SLOTS + 31) / 32; i += EXP_THREADS) sh->seen[i] = sh->twice[i] = 0;
+      for (int i = tid; i < (MAX_IDS + 31) / 32; i += EXP_THREADS) sh->seen[i] = sh->twice[i] = 0;
       __syncthreads();
       for (int s = tid; s < a.n_slots; s += EXP_THREADS) {
         const Slot slot = load_slot<F>(a, s, &bits);
