@@ -525,6 +525,32 @@ def test_zero_tokens_and_another_stream_and_a_graph():
     check_backward(dx, d, mag, x)
 
 
+@gpu
+@pytest.mark.parametrize("T,dtype", [(40, "float32"), (40, "float16"), (4801, "bfloat16")])
+@pytest.mark.parametrize("E,K,n_group,topk_group,group_top", [
+    (64, 6, 1, 1, 1), (128, 8, 1, 1, 1), (200, 12, 1, 1, 1), (256, 8, 1, 1, 1), (384, 1, 1, 1, 1), (1000, 8, 1, 1, 1),
+    (64, 2, 8, 3, 1), (256, 8, 8, 4, 2), (320, 8, 8, 4, 1)])
+def test_zeros_of_either_sign_are_equal(E, K, n_group, topk_group, group_top, T, dtype):
+    """Rows led by a few zeros of mixed signs above distinct negative logits: equal keys, so in the order of their ids,
+    whether they lead or stand at the K-th place."""
+    import torch
+    rng = np.random.default_rng(E + K)
+    lower = -1.0 - np.arange(E) / 128  # distinct, 16-bit types too, down to -8.8
+    if dtype != "float32":
+        lower = -2.0 ** (np.arange(E) // 64 % 10) * (1 + np.arange(E) % 64 / 64)
+    x = np.stack([rng.permutation(lower) for _ in range(T)])
+    for t in range(T):
+        at = rng.choice(E, min(E, 1 + t % (K + 2)), replace=False)
+        x[t, at] = np.where(rng.random(len(at)) < 0.5, 0.0, -0.0)
+    kw = dict(score="softmax", n_group=n_group, topk_group=topk_group, group_top=group_top)
+    xd = torch.from_numpy(x).to(getattr(torch, dtype))
+    ids, w, st = call(xd.cuda(), K, **kw)
+    want_ids, want = ref_router(xd.double().numpy(), K, **kw)
+    assert st == 0
+    np.testing.assert_array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want) <= w_bound(xd.double().numpy(), want, ids, 1.0))
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 
 def test_router_argument_errors():

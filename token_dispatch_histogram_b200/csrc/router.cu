@@ -318,10 +318,6 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
       key[j] = p;
     }
     z = warp_sum(sum);
-    if (!scores) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) key[j] = x[j];
-    }
   }
   *top_logit = m;
   *total = z;
@@ -346,6 +342,10 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
       for (int j = 0; j < NV; ++j)
         if (x[j] == -INFINITY) key[j] = -INFINITY;
     }
+  } else {
+    // -0 becomes +0: they are equal, and the signs of differences below have to say so
+#pragma unroll
+    for (int j = 0; j < NV; ++j) key[j] = x[j] + 0.f;
   }
   // Logits that are there: not past E, nor of a group left out.  The others' keys are -inf.
   uint32_t there = 0xffffffffu;
@@ -358,7 +358,7 @@ __device__ __forceinline__ bool select_fast(const RouterArgs& a, const float (&x
     if (!keep_groups(a, row, scores, &keep)) return false;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (group_scores) key[j] = x[j]; 
+      if (group_scores) key[j] = x[j] + 0.f;
       const uint32_t g = (uint32_t)(lane + 32 * j) * a.group_inv >> 21;
       if (!(keep >> g & 1)) {
         key[j] = -INFINITY;
