@@ -693,8 +693,8 @@ EP_API int ep_router_backward(const float* dw, const void* logits, int dtype, in
  *   - rows outside every slot are neither read into a result nor written;
  *   - bf16 in and out, fp32 sums and activation, one rounding of each result;
  *   - widths (H, I, K, M, N) are multiples of 8; every base is 16-byte aligned;
- *   - a slot with cu_seqlens outside [0, rows] or descending is left out and sets
- *     EP_DEV_BAD_ROW; one with an id past the replicas, or a replica of no
+ *   - a slot with cu_seqlens outside [0, rows] or descending, or that begins before
+ *     the end of an earlier one, is left out and sets EP_DEV_BAD_ROW; one with an id past the replicas, or a replica of no
  *     expert, EP_DEV_BAD_EXPERT_ID; a wait inside the kernel that ran out,
  *     EP_DEV_COPY_TIMEOUT.
  */

@@ -348,6 +348,45 @@ def test_slots_that_do_not_fit_are_left_out_and_flagged():
 
 
 @gpu
+@pytest.mark.parametrize("n", [20, 600])
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("hidden", [False, True])
+def test_slots_that_overlap_are_left_out_and_flagged(hidden, few, n):
+    """Behind an entry of cu_seqlens below the one before it (hidden: at an entry that is no slot) a slot may begin inside
+    an earlier one: of rows that two slots claim, the first has them."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    K, N, E = 64, 136, n
+    # slot 0 [0, 30), 1 goes back, 2 [10, 40) overlaps, 3 [40, 47) and the rest, one row each, do not
+    cu = np.concatenate([[0, 30, 10, 40, 47], 47 + np.arange(1, n - 3)]).astype(np.int32)
+    order = np.arange(n, dtype=np.int32)
+    if hidden:
+        order[1] = -1
+    P = int(cu[-1]) + (0 if few else 8 * n)
+    x, w, wt = values((P, K), 1, True), values((E, N, K), 2, True), values((E, K, N), 3, True)
+    assert few == (P <= 8 * n)  # the form for few rows is chosen by the rows of the buffer
+    to = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    owner = np.full(P, -1)
+    for s in range(n):
+        if s != 1 and s != 2:
+            owner[cu[s]:cu[s + 1]] = s
+    mine = to(owner)
+    for t, weights in ((False, w), (True, wt)):
+        y, st = out((P, N)), status()
+        tdh.ep_expert_gemm(x, weights, to(cu), y, transpose_w=t, slot_order=to(order), dev_status=st)
+        assert tdh.ep_status_read(st) == tdh.EP_DEV_BAD_ROW
+        full = torch.einsum("pk,pnk->pn", x.double(), (weights.transpose(1, 2) if t else weights)[mine.clamp(min=0)]
+                            .double())
+        assert torch.equal(y, torch.where(mine[:, None] >= 0, full, 7.0).to(torch.bfloat16))
+    b, g, st = values((P, 40), 4, True), out((E, K, 40), dtype=torch.float32), status()
+    tdh.ep_expert_wgrad(x, b, to(cu), g, slot_order=to(order), dev_status=st)
+    assert tdh.ep_status_read(st) == tdh.EP_DEV_BAD_ROW
+    for s in [0, 2, 3, 4, n - 1]:
+        r = slice(int(cu[s]), int(cu[s + 1]))
+        assert torch.equal(g[s].double(), x[r].double().T @ b[r].double() if s != 2 else torch.full_like(g[s], 7.0).double())
+
+
+@gpu
 @pytest.mark.parametrize("n", [6, 700])
 def test_an_id_at_two_slots_has_no_gradient_row(n):
     import torch

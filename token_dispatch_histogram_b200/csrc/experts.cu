@@ -150,6 +150,25 @@ __device__ __forceinline__ Slot load_slot(const ExpertArgs& a, int s, int32_t* b
   return r;
 }
 
+// Consecutive slots share their ends, so they can only overlap behind an entry that is below the one before it.  Then a
+// slot with rows that begins before the end of an earlier one (whose id and rows are good) is left out like one that
+// does not fit: two slots would write the same rows, and tiles are counted for disjoint ones.
+__device__ __forceinline__ bool descends(const ExpertArgs& a, int s) {
+  return __ldcg(a.cu + s) > __ldcg(a.cu + s + 1);
+}
+
+template <Form F>
+__device__ __forceinline__ bool overlaps(const ExpertArgs& a, int s) {
+  int32_t ignore = 0;
+  const Slot slot = load_slot<F>(a, s, &ignore);
+  if (slot.len <= 0) return false;
+  for (int o = 0; o < s; ++o) {
+    const Slot other = load_slot<F>(a, o, &ignore);
+    if (other.len > 0 && other.begin + other.len > slot.begin) return true;
+  }
+  return false;
+}
+
 struct Tile {
   Slot slot;
   int m, n;    // first row (within the slot; WGRAD: of the result) and column
@@ -457,7 +476,9 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
       __syncthreads();
     }
     const int nb = (a.N + halves * tn - 1) / (halves * tn);
+    bool down = false;
     for (int s = tid; s < a.n_slots; s += EXP_THREADS) {
+      down |= descends(a, s);
       const Slot slot = load_slot<F>(a, sorted ? sh->sorted[s] : s, &bits);
       int mb = slot.len < 0 ? 0 : ((F == WGRAD ? a.K : slot.len) + TM - 1) / TM;
       if (F == WGRAD && mb && (sh->twice[slot.w >> 5] >> (slot.w & 31) & 1)) {
@@ -465,6 +486,13 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
         mb = 0;
       }
       sh->before[s] = F == WGRAD && a.accumulate && slot.len == 0 ? 0 : mb * nb;
+    }
+    if (__syncthreads_or(down)) {
+      for (int s = tid; s < a.n_slots; s += EXP_THREADS)
+        if (overlaps<F>(a, sorted ? sh->sorted[s] : s)) {
+          bits |= EP_DEV_BAD_ROW;
+          sh->before[s] = 0;
+        }
     }
   }
   if (bits && blockIdx.x == 0) flag(a.dev_status, bits);
@@ -869,9 +897,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   int32_t bits = 0;
   {
     const int nb = (a.N + tn - 1) / tn;
+    bool down = false;
     for (int s = tid; s < a.n_slots; s += FEW_THREADS) {
+      down |= descends(a, s);
       const Slot slot = load_slot<F>(a, s, &bits);
       sh->before[s] = slot.len <= 0 ? 0 : (slot.len + FEW - 1) / FEW * nb;
+    }
+    if (__syncthreads_or(down)) {
+      for (int s = tid; s < a.n_slots; s += FEW_THREADS)
+        if (overlaps<F>(a, s)) {
+          bits |= EP_DEV_BAD_ROW;
+          sh->before[s] = 0;
+        }
     }
   }
   if (bits && blockIdx.x == 0) flag(a.dev_status, bits);
