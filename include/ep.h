@@ -722,7 +722,7 @@ EP_API int ep_expert_up(const uint16_t* x, int64_t rows, int64_t H, const uint16
  * Backward through the second projection and the activation: dgu [rows, 2I] out
  * from dy [rows, H], w2 [n_w, H, I] and the kept gu [rows, 2I]; dh is not
  * rounded in between.  h [rows, I] out (NULL: not wanted) is the activation
- * again, for dW2.
+ * again, for dW2.  dgu may be gu itself; no other output may overlap an input.
  */
 EP_API int ep_expert_up_backward(const uint16_t* dy, int64_t rows, int64_t H, const uint16_t* w2, int n_w, int64_t I,
                                  const uint16_t* gu, const int32_t* cu_seqlens, int n_slots,

@@ -227,6 +227,22 @@ def test_up_backward(lens, H, I, keep):
         check(h, act, rounded(act.abs() * 2 * fast, act, h.dtype), buf, 7.0)
 
 
+@gpu
+@pytest.mark.parametrize("H,I", [(64, 256), (72, 264), (200, 136), (64, 8)])
+@pytest.mark.parametrize("lens", LENS, ids=str)
+def test_up_backward_over_the_kept_products(lens, H, I):
+    """dgu in the place of gu: bit for bit what it is in a place of its own."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    buf = Buffer(LENS[lens])
+    dy, w2, gu = values((buf.P, H), 5), values((buf.E, H, I), 6, scale=H ** -0.5), values((buf.P, 2 * I), 7, scale=3.0)
+    dgu, h, own, kept = out((buf.P, 2 * I)), out((buf.P, I)), out((buf.P, I)), gu.clone()
+    tdh.ep_expert_up_backward(dy, w2, gu, buf.cu, dgu, h, **buf.kw)
+    tdh.ep_expert_up_backward(dy, w2, gu, buf.cu, gu, own, **buf.kw)
+    inside = torch.from_numpy(~buf.outside).cuda()[:, None]
+    assert torch.equal(gu, torch.where(inside, dgu, kept)) and torch.equal(own, h)
+
+
 def wgrad_want(buf, a, b):
     import torch
     n = len(buf.lens)

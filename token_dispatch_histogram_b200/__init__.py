@@ -677,7 +677,8 @@ def ep_expert_up(x, w, cu_seqlens, h, gu=None, slot_order=None, rep_expert=None,
 def ep_expert_up_backward(dy, w2, gu, cu_seqlens, dgu, h=None, slot_order=None, rep_expert=None, dev_status=None,
                           stream=None):
     """dgu [rows, 2I] from dy [rows, H] through w2 [E, H, I] and the activation
-    of the kept gu; h gets the activation again (for w2's gradient)."""
+    of the kept gu; h gets the activation again (for w2's gradient).  dgu may be
+    gu itself."""
     _bf16(dy, w2, gu, dgu, h)
     rows, H = dy.shape
     E, _, I = w2.shape

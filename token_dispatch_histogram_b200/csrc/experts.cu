@@ -344,12 +344,13 @@ __device__ __forceinline__ void store_rows(Turn& t, const float* v, uint16_t* to
   store_rows(t, q, to, ld, rows, n);
 }
 
-// The other way in two steps, so that the loads can be under way early.
+// The other way in two steps, so that the loads can be under way early.  The results may go where these rows come from:
+// a lane then stores what it has loaded itself (Turn gives it the same rows and unit both ways).
 __device__ __forceinline__ void fetch_rows(const Turn& t, uint4* p, const uint16_t* from, int64_t ld, int rows, int n) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     p[j] = make_uint4(0, 0, 0, 0);
-    if (t.row + 8 * j < rows && t.unit * 8 < n) p[j] = ld_stream_v4(from + (t.row + 8 * j) * ld + t.unit * 8);
+    if (t.row + 8 * j < rows && t.unit * 8 < n) p[j] = ld_once_v4(from + (t.row + 8 * j) * ld + t.unit * 8);
   }
 }
 

@@ -156,10 +156,10 @@ class EpLayer:
         return [(g[:, :cut].unflatten(1, (2 * I, H)), g[:, cut:].unflatten(1, (H, I))) for g in (self.g_home, self.g_rep)]
 
     def experts_backward(self, dy, rows, w13, w2, gu, dgu, h, dx, accumulate=False, stream=None):
-        """From dy [P, H]: dgu [P, 2I], h again (both may be overwritten ones of
-        the forward), dx [P, H] (may be dy), and the weights' gradients into
-        g_home and g_rep; rows are the dispatched rows and gu what experts()
-        kept.  grad_reduce() then adds the replicas' to their home's."""
+        """From dy [P, H]: dgu [P, 2I] (may be gu), h again (may be the forward's),
+        dx [P, H] (may be dy), and the weights' gradients into g_home and g_rep;
+        rows are the dispatched rows and gu what experts() kept.  grad_reduce()
+        then adds the replicas' to their home's."""
         kw = dict(dev_status=self.dev_status, stream=stream, **self.slots())
         (home13, home2), (rep13, rep2) = self.weight_grads(w2.shape[2])
         ep_expert_up_backward(dy, w2, gu, dgu=dgu, h=h, **kw)
