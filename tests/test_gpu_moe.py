@@ -191,6 +191,35 @@ def test_autograd_through_the_whole_layer(case):
         assert torch.allclose(got, 2 * was, rtol=1e-5, atol=1e-5 * float(was.abs().max()))
 
 
+def test_a_frozen_trunk_under_trained_experts():
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    from token_dispatch_histogram_b200.autograd import ep_combine_fn, ep_dispatch_fn, ep_experts_fn, ep_router_fn
+    R, S, K, E, H, I = case = 4, 64, 2, 16, 128, 72
+    x, logits, w13, w2, dout = make(*case, seed=7)
+    layer = tdh.EpLayer(R, S, K, E, H, 4, grad_n=3 * H * I)
+    lt = logits.clone().requires_grad_(True)
+    w, ids = ep_router_fn(lt, K, dev_status=layer.dev_status)
+    layer.topk_ids.copy_(ids)
+    layer.route()
+    rows = ep_dispatch_fn(x, layer.pos, K, torch.empty((layer.P, H), dtype=torch.bfloat16, device="cuda"))
+    ep_combine_fn(ep_experts_fn(rows, w13, w2, layer), w, layer.pos).backward(dout)
+    layer.grad_reduce()
+    ref = Model(x, logits, w13, w2, ids, "softmax", 1.0)
+    ref.out.backward(dout.double())
+    (g13, g2), _ = layer.weight_grads(I)
+    close(lt.grad, ref.logits.grad, 4, "dlogits")
+    close(g2, ref.w2.grad, 3, "dw2")
+    close(g13, ref.w13.grad, 3, "dw13")
+    # without gradient rows, and without grad mode, nothing is kept for a backward
+    plain = tdh.EpLayer(R, S, K, E, H, 4)
+    plain.topk_ids.copy_(ids)
+    plain.route()
+    assert not ep_experts_fn(rows, w13, w2, plain).requires_grad
+    with torch.no_grad():
+        assert not ep_experts_fn(rows, w13, w2, layer).requires_grad
+
+
 @pytest.mark.parametrize("planner", ["exact", "quota"])
 def test_a_ranks_slots_cover_its_rows(planner):
     """Each rank's products over its own buffer, with home weights and prefetched replicas' weights, equal the rows of

@@ -17,9 +17,11 @@ for the backward pass ("ŒàŒΩŒ± œÅŒµŒ±ŒªŒπœÉœÑŒπŒ∫œå œÄŒªŒ±ŒØœÉŒπŒø Œ±ŒæŒπŒøŒªœåŒ
 - ep_experts_fn: dispatched rows through a layer's experts; the backward gives
   the rows' gradient and leaves the weights' in the layer's g_home and g_rep, in
   fp32, where grad_reduce and an optimizer take them (the weights are no leaves of
-  the graph).  It saves the rows and the plan's slots by reference: both must stay
-  as they are until the backward (a buffer and a layer of their own, not the next
-  step's).
+  the graph).  So its backward has to run wherever the layer holds such rows:
+  then its result requires a gradient even if the rows do not (a frozen trunk
+  under trained experts), and backward() reaches it.  It saves the rows and the
+  plan's slots by reference: both must stay as they are until the backward (a
+  buffer and a layer of their own, not the next step's).
 
 Every step runs in libep.so's kernels; these classes only allocate outputs and
 route tensors.
@@ -87,7 +89,7 @@ class _Router(torch.autograd.Function):
 
 class _Experts(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, rows, w13, w2, layer, accumulate):
+    def forward(ctx, rows, w13, w2, layer, accumulate, anchor):
         P, I = rows.shape[0], w2.shape[2]
         like = dict(dtype=torch.bfloat16, device=rows.device)
         h, gu, y = torch.empty((P, I), **like), torch.empty((P, 2 * I), **like), torch.empty(rows.shape, **like)
@@ -105,7 +107,7 @@ class _Experts(torch.autograd.Function):
         h = torch.empty((gu.shape[0], gu.shape[1] // 2), dtype=gu.dtype, device=gu.device)
         dx = torch.zeros_like(rows)  # rows of no slot get no gradient
         ctx.layer.experts_backward(dy.contiguous(), rows, w13, w2, gu, dgu, h, dx, ctx.accumulate)
-        return dx, None, None, None, None
+        return dx, None, None, None, None, None
 
 
 def ep_router_fn(logits, K, dev_status=None, **kw):
@@ -118,8 +120,13 @@ def ep_experts_fn(rows, w13, w2, layer, accumulate=False):
     """y = the rows [P, H] of a layer's dispatch through its experts (w13
     [E, 2I, H], w2 [E, H, I], over the layer's current plan).  The backward gives
     drows, and the weights' gradients into layer.g_home and layer.g_rep (added
-    to what is there if accumulate)."""
-    return _Experts.apply(rows, w13, w2, layer, accumulate)
+    to what is there if accumulate).  If the layer has those (grad_n = 3*H*I), y
+    requires a gradient whether rows do or not; torch.autograd.grad() towards
+    inputs that rows do not depend on leaves the weights' gradients out."""
+    # a leaf that nobody sees makes autograd run the backward for the weights alone
+    trained = torch.is_grad_enabled() and layer.grad_n == 3 * layer.H * w2.shape[2]
+    anchor = torch.empty(0, device=rows.device, requires_grad=True) if trained else None
+    return _Experts.apply(rows, w13, w2, layer, accumulate, anchor)
 
 
 def ep_dispatch_fn(x, pos, K, buf):
