@@ -110,6 +110,8 @@ extern "C" {
 #define EP_DTYPE_BF16 1
 #define EP_DTYPE_F16 2 /* router logits only */
 
+#define EP_ACCUMULATE_HOME 2 /* ep_expert_wgrad's accumulate: the home rows only */
+
 #define EP_SCORE_SOFTMAX 0
 #define EP_SCORE_SIGMOID 1
 
@@ -738,6 +740,9 @@ EP_API int ep_expert_up_backward(const uint16_t* dy, int64_t rows, int64_t H, co
  *   rep_dtype   of g_rep, EP_DTYPE_F32 or EP_DTYPE_BF16.
  *   accumulate  != 0: added to what is there (one fp32 add; bf16 rows rounded
  *               again); otherwise written, zeros for a slot without rows.
+ *               EP_ACCUMULATE_HOME: added in the home rows, written in the replicas'
+ *               (a reduction has taken what stood there, or it belongs to another
+ *               plan's replicas).
  * Rows of g_home and g_rep that belong to no slot are left as they are.  An id that
  * stands at two slots has no row of its own: both are left out, with
  * EP_DEV_BAD_EXPERT_ID.  ld_home and ld_rep are at

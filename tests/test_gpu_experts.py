@@ -286,6 +286,20 @@ def test_wgrad(lens, M, N, rep_dtype, accumulate, ints):
 
 
 @gpu
+@pytest.mark.parametrize("rep_dtype", ["float32", "bfloat16"])
+def test_wgrad_added_to_the_home_rows_only(rep_dtype):
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    buf = Buffer([40, 0, 129, 3, 70, 0])  # the last two are replicas
+    a, b = values((buf.P, 136), 1, True), values((buf.P, 72), 2, True)
+    home, rep = out((buf.E, 136, 72), 3.0, torch.float32), out((buf.reps, 136, 72), 3.0, getattr(torch, rep_dtype))
+    tdh.ep_expert_wgrad(a, b, buf.cu, home, rep, accumulate="home", **buf.kw)
+    want, _ = wgrad_want(buf, a, b)
+    assert torch.equal(home.double(), want[:buf.E] + 3.0)
+    assert torch.equal(rep, want[buf.E:].to(rep.dtype))
+
+
+@gpu
 def test_rows_of_other_slots_take_no_part():
     """An infinity or NaN in one slot's rows stays in that slot: in the products' rows and in the weight gradients,
     whose last block of rows reaches into the next slot's."""
@@ -670,3 +684,11 @@ def test_expert_binding_refuses_wrong_tensors():
         tdh.ep_expert_wgrad(x, y, cu, torch.zeros(2, 64, 72, **bf))
     with pytest.raises(ValueError):
         tdh.ep_expert_wgrad(x, y, cu, torch.zeros(2, 72, 64))
+
+
+def test_wgrad_refuses_another_word_for_accumulate():
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    x, y = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 72, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="accumulate"):
+        tdh.ep_expert_wgrad(x, y, torch.zeros(3, dtype=torch.int32), torch.zeros(2, 64, 72), accumulate="replicas")

@@ -220,6 +220,40 @@ def test_a_frozen_trunk_under_trained_experts():
         assert not ep_experts_fn(rows, w13, w2, layer).requires_grad
 
 
+def test_micro_batches_that_are_each_reduced():
+    """Three micro-batches of their own routing: the sum of three separate gradients, replicas counted once each."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    R, S, K, E, H, I = case = 4, 64, 2, 16, 128, 72
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    layer = tdh.EpLayer(R, S, K, E, H, 4, grad_n=3 * H * I)
+    P = layer.P
+    h, gu, y = torch.empty((P, I), **bf), torch.empty((P, 2 * I), **bf), torch.empty((P, H), **bf)
+    dy, dgu, dx, dw = (torch.empty((P, H), **bf), torch.empty((P, 2 * I), **bf), torch.empty((P, H), **bf),
+                       torch.empty((R * S, K), device="cuda"))
+    _, _, w13, w2, _ = make(*case)
+
+    def backward(seed, accumulate):
+        x, logits, _, _, dout = make(*case, seed=seed)
+        layer.x.copy_(x)
+        layer.router(logits)
+        layer.route()
+        assert layer.plan_view("n_rep", 1).item() > 0
+        layer.dispatch()
+        layer.experts(w13, w2, h, gu, y)
+        tdh.ep_combine_backward(dout, layer.w, y, layer.pos, dy, dw, layer.dev_status)
+        layer.experts_backward(dy, layer.buf, w13, w2, gu, dgu, h, dx, accumulate=accumulate)
+        layer.grad_reduce()
+        assert layer.status() == 0
+        return layer.g_home.clone()
+
+    want = sum(backward(seed, False).double() for seed in (1, 2, 3))
+    backward(1, False)
+    backward(2, True)
+    got = backward(3, True)
+    assert float((got.double() - want).norm() / want.norm()) <= 1e-6
+
+
 @pytest.mark.parametrize("planner", ["exact", "quota"])
 def test_a_ranks_slots_cover_its_rows(planner):
     """Each rank's products over its own buffer, with home weights and prefetched replicas' weights, equal the rows of

@@ -27,6 +27,7 @@ EP_MAX_EXPERTS = 1024
 EP_MAX_RANKS = 1024
 EP_DTYPE_F32, EP_DTYPE_BF16, EP_DTYPE_F16 = 0, 1, 2
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_ACCUMULATE_HOME = 2
 EP_IPC_HANDLE_BYTES = 64
 
 
@@ -706,8 +707,12 @@ def ep_expert_wgrad(a, b, cu_seqlens, g_home, g_rep=None, accumulate=False, slot
                     dev_status=None, stream=None):
     """a_s^T b_s of every slot s, into g_home[e] (home copies) and g_rep[m]
     (replica m); g_home [E, M, N] fp32 and g_rep [cap, M, N] fp32 or bf16 may be
-    parts of longer rows (a stride between experts).  rep_expert is not read: a
+    parts of longer rows (a stride between experts).  accumulate: False, True, or
+    "home" (added in g_home, written in g_rep).  rep_expert is not read: a
     replica's gradient has its own row."""
+    mode = EP_ACCUMULATE_HOME if accumulate == "home" else int(bool(accumulate))
+    if isinstance(accumulate, str) and accumulate != "home":
+        raise ValueError(f"accumulate {accumulate!r}, expected False, True or 'home'")
     _bf16(a, b)
     _dtype(g_home, torch.float32)
     rows, M = a.shape
@@ -722,7 +727,7 @@ def ep_expert_wgrad(a, b, cu_seqlens, g_home, g_rep=None, accumulate=False, slot
         dt = EP_DTYPE_F32 if g_rep.dtype == torch.float32 else EP_DTYPE_BF16
     cu, n, order, _, _ = _slots(cu_seqlens, slot_order, None)
     _launch("ep_expert_wgrad", (_at(a), _at(b), rows, M, N, cu, n, order, home, g_home.shape[0], ld_home, rep, dt,
-                                n_rep, ld_rep, bool(accumulate), _at(dev_status)), stream, a, b, cu_seqlens, g_home,
+                                n_rep, ld_rep, mode, _at(dev_status)), stream, a, b, cu_seqlens, g_home,
             g_rep, slot_order, dev_status)
 
 

@@ -119,8 +119,9 @@ def ep_router_fn(logits, K, dev_status=None, **kw):
 def ep_experts_fn(rows, w13, w2, layer, accumulate=False):
     """y = the rows [P, H] of a layer's dispatch through its experts (w13
     [E, 2I, H], w2 [E, H, I], over the layer's current plan).  The backward gives
-    drows, and the weights' gradients into layer.g_home and layer.g_rep (added
-    to what is there if accumulate).  If the layer has those (grad_n = 3*H*I), y
+    drows, and the weights' gradients into layer.g_home (added to what is there
+    if accumulate) and layer.g_rep, which layer.grad_reduce() takes after each
+    backward.  If the layer has those (grad_n = 3*H*I), y
     requires a gradient whether rows do or not; torch.autograd.grad() towards
     inputs that rows do not depend on leaves the weights' gradients out."""
     # a leaf that nobody sees makes autograd run the backward for the weights alone

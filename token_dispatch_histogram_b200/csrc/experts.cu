@@ -111,7 +111,7 @@ struct ExpertArgs {
   float* g_home;
   void* g_rep;
   int64_t ld_home, ld_rep;  // elements between experts
-  bool rep_bf16, accumulate;
+  bool rep_bf16, add_home, add_rep;  // add: to what is there
   uint64_t wait_ns;  // the bound of a wait: a second, and more where a tile may take long
   int32_t* dev_status;
 };
@@ -383,7 +383,7 @@ __device__ __forceinline__ void store_grad(Turn& t, const ExpertArgs& a, int id,
         if (t.row + 8 * j < rows && c + t.unit * 4 < n) {
           float* q = to + (int64_t)(t.row + 8 * j) * a.N + c + t.unit * 4;
           uint4 s = t.theirs(j);
-          if (a.accumulate) {
+          if (home ? a.add_home : a.add_rep) {
             const float4 o = *reinterpret_cast<const float4*>(q);
             s = make_uint4(__float_as_uint(o.x + __uint_as_float(s.x)), __float_as_uint(o.y + __uint_as_float(s.y)),
                            __float_as_uint(o.z + __uint_as_float(s.z)), __float_as_uint(o.w + __uint_as_float(s.w)));
@@ -396,7 +396,7 @@ __device__ __forceinline__ void store_grad(Turn& t, const ExpertArgs& a, int id,
     uint16_t* to = (uint16_t*)a.g_rep + (int64_t)(id - a.n_w) * a.ld_rep + at;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (a.accumulate && t.row + 8 * j < rows && t.unit * 8 < n)
+      if (a.add_rep && t.row + 8 * j < rows && t.unit * 8 < n)
         t.theirs(j) = *reinterpret_cast<const uint4*>(to + (int64_t)(t.row + 8 * j) * a.N + t.unit * 8);
     __syncwarp();
 #pragma unroll
@@ -404,7 +404,7 @@ __device__ __forceinline__ void store_grad(Turn& t, const ExpertArgs& a, int id,
       float o[8];
       unpack8(t.mine(u), o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = a.accumulate ? o[i] + v[8 * u + i] : v[8 * u + i];
+      for (int i = 0; i < 8; ++i) o[i] = a.add_rep ? o[i] + v[8 * u + i] : v[8 * u + i];
       t.mine(u) = pack8(o);
     }
     __syncwarp();
@@ -486,7 +486,8 @@ __global__ void __launch_bounds__(EXP_THREADS, 1) __cluster_dims__(2, 1, 1)
         bits |= EP_DEV_BAD_EXPERT_ID;
         mb = 0;
       }
-      sh->before[s] = F == WGRAD && a.accumulate && slot.len == 0 ? 0 : mb * nb;
+      if (F == WGRAD && slot.len == 0 && (slot.w < a.n_w ? a.add_home : a.add_rep)) mb = 0;  // nothing to add
+      sh->before[s] = mb * nb;
     }
     if (__syncthreads_or(down)) {
       for (int s = tid; s < a.n_slots; s += EXP_THREADS)
@@ -1177,7 +1178,8 @@ extern "C" int ep_expert_wgrad(const uint16_t* a_rows, const uint16_t* b_rows, i
   ExpertArgs a = {};
   a.rows = rows, a.N = (int)N, a.K = (int)M, a.n_slots = n_slots, a.n_w = n_home, a.n_rep = g_rep ? n_rep : 0;
   a.cu = cu_seqlens, a.slots = slot_order, a.g_home = g_home, a.g_rep = g_rep, a.ld_home = ld_home, a.ld_rep = ld_rep;
-  a.rep_bf16 = rep_dtype == EP_DTYPE_BF16, a.accumulate = accumulate != 0, a.dev_status = dev_status;
+  a.rep_bf16 = rep_dtype == EP_DTYPE_BF16, a.dev_status = dev_status;
+  a.add_home = accumulate != 0, a.add_rep = accumulate != 0 && accumulate != EP_ACCUMULATE_HOME;
   CUtensorMap ma, mb;
   // without rows nothing is read, but a map needs an address
   if (!map_rows(&ma, rows ? (const void*)a_rows : g_home, rows ? rows : 1, (int)M, TK) ||

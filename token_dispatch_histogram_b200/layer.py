@@ -159,7 +159,10 @@ class EpLayer:
         """From dy [P, H]: dgu [P, 2I] (may be gu), h again (may be the forward's),
         dx [P, H] (may be dy), and the weights' gradients into g_home and g_rep;
         rows are the dispatched rows and gu what experts() kept.  grad_reduce()
-        then adds the replicas' to their home's."""
+        then adds the replicas' to their home's: after every backward, since the
+        replicas are the plan's.  accumulate adds to g_home; g_rep is written
+        anew all the same, what stood there has been reduced."""
+        accumulate = "home" if accumulate else False
         kw = dict(dev_status=self.dev_status, stream=stream, **self.slots())
         (home13, home2), (rep13, rep2) = self.weight_grads(w2.shape[2])
         ep_expert_up_backward(dy, w2, gu, dgu=dgu, h=h, **kw)
