@@ -768,7 +768,14 @@ EP_API int ep_expert_wgrad(const uint16_t* a, const uint16_t* b, int64_t rows, i
  *     its root.  scale = largest * (1 / 448), largest the block's largest magnitude;
  *     codes are value * (448 * (1 / largest)) rounded to nearest even; a nonzero
  *     root gets at least the smallest code; a block with no magnitude above 2^-100
- *     is held as zeros.
+ *     is held as zeros.  Once (1 - b2) / (1 - b2^t) < 1/32 a step hardly ever moves a
+ *     root by half a code, and rounded to nearest it would stand still: from then
+ *     on roots that were not 0 are rounded to one of the two codes around them by
+ *     chance, in proportion, so that they follow v on average.  The chance comes of
+ *     t, the tensor's place in the table and the element's in the tensor; equal
+ *     calls give equal codes.  (Above that share roots follow gradients that vary
+ *     from step to step; of gradients that do not vary at all, those that grow or
+ *     fall against the rest of their block by less than a step can show stay.)
  *     p is computed before the moments are coded.  Zeroed codes and scales are a
  *     fresh state.  A NaN keeps to its element; an infinity takes its block along.
  * All pointers of a tensor are device pointers of its own; t.p, t.m, t.v, the

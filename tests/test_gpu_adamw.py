@@ -368,6 +368,82 @@ def test_another_stream_and_going_on_from_a_state():
     assert torch.equal(q, case.p[0]) and int(c.steps) == 2 and torch.equal(c.m[0], a.m[0])
 
 
+@gpu
+@pytest.mark.parametrize("noisy", [False, True])
+@pytest.mark.parametrize("change", [5.0, 0.2])
+@pytest.mark.parametrize("beta2,steps", [(0.99, 600), (0.999, 3000)])
+def test_moments_in_8_bits_follow_those_in_32(beta2, steps, change, noisy):
+    """Half of the gradients change their size for good, and the 8-bit roots follow as the fp32 ones do.
+
+    With c = 1 - beta2, a step moves a root r by c/2 (k - 1) r, k = g^2 / v (E|k - 1| < 1), so its code by chance: a
+    variance of at most c/2 r * r/8 a step (a code is at most r/8), which decays at 2 c a step: 0.18 r in all, twice that
+    while k is not 1.  Rounding by chance has no bias; that of a root of noisy v is half the variance, 2 %."""
+    import torch
+    from token_dispatch_histogram_b200.optim import EpAdamW
+    n = 256 * 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    size = torch.exp(torch.randn(n, generator=g, device="cuda"))
+    moved = torch.rand(n, generator=g, device="cuda") < 0.5
+    grad = torch.empty(n, device="cuda")
+    a, b = (EpAdamW([torch.zeros(n, device="cuda")], [grad], lr=1e-6, betas=(0.9, beta2), weight_decay=0.0,
+                    state_bits=bits) for bits in (8, 32))
+    for t in range(2 * steps):
+        grad.copy_(size * torch.randn(n, generator=g, device="cuda") if noisy else size)
+        if t >= steps:
+            grad[moved] *= change
+        a.step()
+        b.step()
+    ratio = a.v[0].float() * a.v_scale[0].repeat_interleave(BLOCK) / b.v[0].sqrt()
+    for part in (ratio[moved], ratio[~moved]):
+        assert 0.9 <= float(part.mean()) <= 1.1 and float(part.std()) <= 0.36
+
+
+@gpu
+@pytest.mark.parametrize("off,n", [(0, 256 * 400), (3, 70_001)])
+def test_roots_are_rounded_by_chance_where_steps_are_small(off, n):
+    """Far into a run each root goes to one of the two codes around it, in proportion; all else is as before."""
+    import torch
+    b2 = 0.999
+    cases = [Case([300, n], 8, off=off, spread=1.0) for _ in range(2)]
+    opts = [c.make(lr=1e-2, betas=(0.9, b2), eps=1e-8, weight_decay=0.1) for c in cases]
+    for c, o in zip(cases, opts):
+        for _ in range(3):  # still to nearest: 0.001 / (1 - 0.999^t) is near 1 / t
+            o.step()
+        c.step.fill_(1000)
+        c.new_grads()
+        c.g[1][7::1000] = 0.0
+    s = cases[0].numpy()
+    con = constants(1001, 1e-2, 0.9, b2, 1e-8, 0.1)
+    want = ref_step(s, 8, con)
+    for o in opts:
+        o.step()
+    got, other = (c.numpy() for c in cases)
+    for k in ("p", "m", "v", "ms", "vs"):
+        for i in range(2):
+            np.testing.assert_array_equal(np.asarray(got[k][i]), np.asarray(other[k][i]))  # the same chance
+            if k != "v":
+                np.testing.assert_array_equal(np.asarray(got[k][i]), np.asarray(want[k][i]))
+    cases[0].outside_is_untouched()
+    v = ref_decode(s["v"][1], s["vs"][1])
+    root = ref_update(s["p"][1], s["g"][1], np.zeros_like(v), v * v, con)[3].astype(np.float64)
+    vs = np.repeat(got["vs"][1], BLOCK)[:n].astype(np.float64)
+    z = root / vs  # in units of the codes' values; 3 roundings of fp32 off what the kernel rounds
+    held = got["v"][1].view(torch.float8_e4m3fn).double().numpy()
+    unit = 2.0 ** np.maximum(np.floor(np.log2(z)) - 3, -9)
+    assert np.all(np.abs(held - z) <= unit * (1 + 2.0 ** -15)) and np.all(held > 0)
+    # those above the smallest code and below the largest: no bias, within five deviations of a mean of n (1/2 each at most)
+    sel = (z > 2.0 ** -9) & (z < 447)
+    assert abs(np.mean(((held - z) / unit)[sel])) <= 5 * 0.5 / np.sqrt(sel.sum())
+    # and by chance indeed: farther than half a code as often as that says, 1/4 if places in between are evenly taken
+    assert 0.2 <= np.mean((np.abs(held - z) > unit / 2)[sel]) <= 0.3
+    # another step, another chance
+    for c, t in zip(cases, (1000, 1001)):
+        c.step.fill_(t)
+    for o in opts:
+        o.step()
+    assert not torch.equal(cases[0].v[1], cases[1].v[1])
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 
 def test_adamw_argument_errors():

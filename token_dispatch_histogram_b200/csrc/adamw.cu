@@ -10,6 +10,17 @@
 // code 0, which a later step would divide by.  A step computes with the moments
 // before they are coded again.
 //
+// A step moves v by the share c = (1 - b2) / (1 - b2^t) of g^2 - v at most.  A
+// code is 6 to 12 % of a root: rounded to nearest, roots stand still once c is so
+// small that hardly a step moves one by half of that (b2 = 0.999, half of the
+// gradients changed fivefold: 3000 steps later their roots were a third, or three
+// times, of fp32's).  From c < 1/32 on, roots that had a value are therefore
+// rounded up or down by chance, in proportion, so that they follow v on average
+// (0.99 to 1.02 of fp32's there, 15 to 25 % around it).  The chance is a hash of
+// step and element: the same step gives the same codes.  The first moment's share
+// is 1 - b1 of a gradient that is mostly noise, which moves its codes; it is
+// rounded to nearest.
+//
 // Every product, sum, quotient and root is rounded by itself, in the order
 // above, so the codes do not depend on how a compiler joins operations.
 //
@@ -47,7 +58,19 @@ struct AdamArgs {
 // What the elements need of the step, in fp32: computed once per CTA in fp64.
 struct AdamConst {
   float b1, b2, c1m, c2m, decay, c1, c2, eps, gs;
+  uint32_t chance;  // 8 bits: a seed of this step's roundings, or 0: to nearest
 };
+
+constexpr double NEAREST_SHARE = 1.0 / 32;  // of g^2 in v, down to which roots are rounded to nearest
+
+// A bijection of 32 bits that spreads each bit over all (xorshift and multiply steps).
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x7feb352du;
+  x ^= x >> 15;
+  x *= 0x846ca68bu;
+  return x ^ x >> 16;
+}
 
 __device__ __forceinline__ AdamConst adam_const(const AdamArgs& a) {
   const double t = *a.step, lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
@@ -58,7 +81,9 @@ __device__ __forceinline__ AdamConst adam_const(const AdamArgs& a) {
   c.c2m = (float)(1.0 - a.b2);
   c.decay = (float)(1.0 - lr * a.wd);
   c.c1 = (float)(lr / (1.0 - pow(a.b1, t)));
-  c.c2 = (float)(1.0 / sqrt(1.0 - pow(a.b2, t)));
+  const double part = 1.0 - pow(a.b2, t);
+  c.c2 = (float)(1.0 / sqrt(part));
+  c.chance = 1.0 - a.b2 < NEAREST_SHARE * part ? mix32((uint32_t)*a.step) | 1u : 0u;
   c.eps = (float)a.eps;
   c.gs = a.grad_scale ? *a.grad_scale : 1.f;
   return c;
@@ -143,9 +168,18 @@ __device__ __forceinline__ void load8_codes(const uint8_t* p, int64_t i, int64_t
   }
 }
 
-// Codes of a block's eight values a lane, and the block's scale (the same on every lane).
-template <bool ROOT>
-__device__ __forceinline__ float store8_codes(uint8_t* p, int64_t i, int64_t n, bool vec, const float* x) {
+// A positive value below 480 to one of its two neighbours among the codes' values, `bits` (20 of them) being the chance:
+// added below the last place that a code holds, then cut off there.  Below 2^-6 the codes are multiples of 2^-9.
+__device__ __forceinline__ float round_by_chance(float y, uint32_t bits) {
+  if (y < 0x1p-6f) return floorf(fmaf(y, 0x1p9f, (float)bits * 0x1p-20f)) * 0x1p-9f;
+  return __uint_as_float((__float_as_uint(y) + bits) & 0xfff00000u);
+}
+
+// Codes of a block's eight values a lane, and the block's scale (the same on every lane).  CHANCE: those of the eight
+// that `had` a value before are rounded by the lane's chance, otherwise to nearest.
+template <bool ROOT, bool CHANCE>
+__device__ __forceinline__ float store8_codes(uint8_t* p, int64_t i, int64_t n, bool vec, const float* x,
+                                              uint32_t chance, uint32_t had) {
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));  // a NaN keeps to its own element
@@ -160,6 +194,7 @@ __device__ __forceinline__ float store8_codes(uint8_t* p, int64_t i, int64_t n, 
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       y[k] = __fmul_rn(x[j + k], inv);
+      if (CHANCE && (had >> (j + k) & 1) && y[k] < 480.f) y[k] = round_by_chance(y[k], mix32(chance + j + k) >> 12);
       if (ROOT && x[j + k] > 0.f && y[k] < FP8_MIN) y[k] = FP8_MIN;
     }
     const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
@@ -175,15 +210,9 @@ __device__ __forceinline__ float store8_codes(uint8_t* p, int64_t i, int64_t n, 
   return held ? __fmul_rn(top, 1.f / FP8_MAX) : 0.f;
 }
 
-template <bool EIGHT, bool GRAD_BF16, int CAP>
-__global__ void __launch_bounds__(ADAM_WARPS * 32, 4)
-    k_adamw(const __grid_constant__ AdamTable<CAP> tab, const __grid_constant__ AdamArgs a) {
-  __shared__ AdamConst s_c;
-  wait_for_predecessor();
-  if (threadIdx.x == 0) s_c = adam_const(a);
-  __syncthreads();
-  const AdamConst c = s_c;
-  const bool scaled = a.grad_scale != nullptr;
+// CHANCE: the roots' codes are rounded by chance in this step (8 bits only).
+template <bool EIGHT, bool GRAD_BF16, bool CHANCE, int CAP>
+__device__ __forceinline__ void adam_blocks(const AdamTable<CAP>& tab, const AdamConst& c, bool scaled) {
   const int lane = threadIdx.x & 31;
   const int total = tab.before[tab.n];
   int k = 0;  // the tensor of the block at hand; blocks come in ascending order
@@ -201,6 +230,7 @@ __global__ void __launch_bounds__(ADAM_WARPS * 32, 4)
     const int64_t block = b - tab.before[k], i = block * ADAM_BLOCK + lane * 8, n = t.n;
     const bool vec = t.vec != 0;
     float p[8], g[8], m[8], v[8], root[8];
+    uint32_t had = 0;
     load8((const float*)t.p, i, n, vec, p);
     if (GRAD_BF16)
       load8_bf16((const uint16_t*)t.g, i, n, vec, g);
@@ -210,7 +240,10 @@ __global__ void __launch_bounds__(ADAM_WARPS * 32, 4)
       load8_codes((const uint8_t*)t.m, i, n, vec, t.m_scale[block], m);
       load8_codes((const uint8_t*)t.v, i, n, vec, t.v_scale[block], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+      for (int j = 0; j < 8; ++j) {
+        if (CHANCE) had |= v[j] > 0.f ? 1u << j : 0u;
+        v[j] = __fmul_rn(v[j], v[j]);
+      }
     } else {
       load8((const float*)t.m, i, n, vec, m);
       load8((const float*)t.v, i, n, vec, v);
@@ -221,8 +254,9 @@ __global__ void __launch_bounds__(ADAM_WARPS * 32, 4)
     if (t.copy) store8_bf16((uint16_t*)t.copy, i, n, vec, p);
     if (EIGHT) {
       // elements behind the tensor's end are 0 all along, and a 0 gradient keeps them so
-      const float ms = store8_codes<false>((uint8_t*)t.m, i, n, vec, m);
-      const float vs = store8_codes<true>((uint8_t*)t.v, i, n, vec, root);
+      const float ms = store8_codes<false, false>((uint8_t*)t.m, i, n, vec, m, 0, 0);
+      const uint32_t chance = CHANCE ? mix32(mix32(c.chance + (uint32_t)k) + (uint32_t)(i >> 3)) << 3 : 0u;
+      const float vs = store8_codes<true, CHANCE>((uint8_t*)t.v, i, n, vec, root, chance, had);
       if (lane == 0) {
         t.m_scale[block] = ms;
         t.v_scale[block] = vs;
@@ -232,6 +266,21 @@ __global__ void __launch_bounds__(ADAM_WARPS * 32, 4)
       store8((float*)t.v, i, n, vec, v);
     }
   }
+}
+
+template <bool EIGHT, bool GRAD_BF16, int CAP>
+__global__ void __launch_bounds__(ADAM_WARPS * 32, 4)
+    k_adamw(const __grid_constant__ AdamTable<CAP> tab, const __grid_constant__ AdamArgs a) {
+  __shared__ AdamConst s_c;
+  wait_for_predecessor();
+  if (threadIdx.x == 0) s_c = adam_const(a);
+  __syncthreads();
+  const AdamConst c = s_c;
+  const bool scaled = a.grad_scale != nullptr;
+  if (EIGHT && c.chance)
+    adam_blocks<EIGHT, GRAD_BF16, EIGHT, CAP>(tab, c, scaled);
+  else
+    adam_blocks<EIGHT, GRAD_BF16, false, CAP>(tab, c, scaled);
 }
 
 template <int CAP>

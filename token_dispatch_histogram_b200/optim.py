@@ -19,6 +19,9 @@ class EpAdamW:
         fp32 or all bf16, read at every step; copies: bf16 tensors (or None
         each) that get the rounded parameters.  lr: a number, or an fp32 CUDA
         tensor of one element that a captured step reads again at every replay.
+        state_bits 8: the second moment's root is rounded to nearest in the first
+        steps and up to beta2 = 0.968, beyond by chance (the same for the same
+        step), since steps so small would never move a code: see ep.h.
         state: a state_dict() to go on from (its tensors are used, not copied);
         otherwise the moments start at zero."""
         if state_bits not in (8, 32):
