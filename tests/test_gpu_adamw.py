@@ -444,6 +444,28 @@ def test_roots_are_rounded_by_chance_where_steps_are_small(off, n):
     assert not torch.equal(cases[0].v[1], cases[1].v[1])
 
 
+@gpu
+def test_a_refused_step_does_not_count():
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    case = Case([100], 32)
+    opt = case.make(lr=1e-2)
+    opt.step()
+    for bad, err in ((dict(grad_scale=torch.ones(1, dtype=torch.float64, device="cuda")), TypeError),
+                     (dict(grad_scale=torch.ones(2, device="cuda")), ValueError),
+                     (dict(grad_scale=torch.ones(1)), ValueError)):
+        with pytest.raises(err):
+            opt.step(**bad)
+        assert int(case.step) == 1
+    opt.lr = float("nan")
+    with pytest.raises(tdh.EpError):
+        opt.step()
+    assert int(case.step) == 1
+    opt.lr = 1e-2
+    opt.step()
+    assert int(case.step) == 2
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 
 def test_adamw_argument_errors():

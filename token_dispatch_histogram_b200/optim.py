@@ -66,14 +66,22 @@ class EpAdamW:
 
     def step(self, grad_scale=None, stream=None):
         """One step from the gradients as they are now; grad_scale: fp32 CUDA
-        tensor of one element that multiplies them (a clipping factor)."""
+        tensor of one element that multiplies them (a clipping factor).  A call
+        that is refused does not count as a step."""
+        self._count(1, stream)
+        try:
+            ep_adamw(self._table, len(self.params), self.state_bits, self._grad_dtype, self.steps, self.lr, self.betas,
+                     self.eps, self.weight_decay, grad_scale, stream)
+        except Exception:
+            self._count(-1, stream)
+            raise
+
+    def _count(self, n, stream):
         if stream is None:
-            self.steps.add_(1)
+            self.steps.add_(n)
         else:
             with torch.cuda.stream(stream):
-                self.steps.add_(1)
-        ep_adamw(self._table, len(self.params), self.state_bits, self._grad_dtype, self.steps, self.lr, self.betas,
-                 self.eps, self.weight_decay, grad_scale, stream)
+                self.steps.add_(n)
 
     def state_dict(self):
         """The state's own tensors (not copies)."""
