@@ -551,6 +551,75 @@ def test_zeros_of_either_sign_are_equal(E, K, n_group, topk_group, group_top, T,
     assert np.all(np.abs(w - want) <= w_bound(xd.double().numpy(), want, ids, 1.0))
 
 
+@gpu
+@pytest.mark.parametrize("kind", ["logits", "bias", "infinite"])
+def test_a_group_that_is_left_out_costs_nothing(kind):
+    """One group without an expert to take (its logits masked, or its biases -inf), or with a key of +inf, does not send
+    every token through fp64, which takes many times as long: the time stays near that of the batch without it."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    T, E, K = 65536, 256, 8
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn((T, E), generator=g, device="cuda")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    x2, bias2 = x.clone(), bias.clone()
+    if kind == "logits":
+        x2[:, 32:64] = -float("inf")
+    elif kind == "bias":
+        bias2[32:64] = -float("inf")
+    else:
+        bias2[40] = float("inf")
+    ids, w = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
+
+    def best(x, b):
+        times = []
+        for _ in range(8):
+            a, z = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                tdh.ep_router(x, ids, w, score="sigmoid", bias=b, n_group=8, topk_group=4, group_top=2)
+            z.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(z))
+        return min(times)
+
+    plain, other = best(x, bias), best(x2, bias2)
+    assert other <= 2 * plain
+
+
+@gpu
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_of_infinite_keys(score, group_top):
+    """Groups masked by logits or by biases, with infinite biases, and with finite biases whose sum is too large for fp32:
+    the order is that of the definition."""
+    import torch
+    T, E, K, n_group = 60, 128, 6, 8
+    x = logits_of(T, E, torch.float32, 5)
+    rng = np.random.default_rng(6)
+    top = float(np.finfo(np.float32).max)
+    for kind in range(6):
+        bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+        y = x.clone()
+        if kind in (0, 5):
+            y[:, 16:32] = -float("inf")
+        if kind in (1, 5):
+            bias[32:48] = -np.inf
+        if kind in (2, 5):
+            bias[[50, 70]] = np.inf
+        if kind in (3, 5):
+            bias[[80, 81, 96, 97]] = top * np.array([0.8, 0.8, 0.9, 0.9])
+        if kind in (4, 5):
+            bias[112:128] = -top
+            bias[2:4] = -top
+        for topk_group in (2, 5, 7):
+            kw = dict(score=score, n_group=n_group, topk_group=topk_group, group_top=group_top)
+            ids, w, st = call(y.cuda(), K, bias=bias, **kw)
+            with np.errstate(over="ignore"):
+                want_ids, want = ref_router(y.double().numpy(), K, bias=bias.astype(np.float64), **kw)
+            np.testing.assert_array_equal(ids, want_ids)
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 
 def test_router_argument_errors():

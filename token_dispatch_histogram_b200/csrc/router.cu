@@ -266,25 +266,29 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* ro
     first = fmaxf(first, f);
   }
   // off: what the score may be off, from its keys' errors (s is at most 1; the keys may be large and cancel) and the
-  // sum's rounding
+  // sum's rounding.  An infinite key is so in truth (no expert left, or an infinite bias), and its group's score with it;
+  // an infinite sum of finite keys is not.
   float score = first, off = key_error(a.sigmoid, 1.f, first);
   if (a.group_top == 2 && second != -INFINITY) {
     score += second;
     off += key_error(a.sigmoid, 1.f, second) + 1.2e-7f * fabsf(score);
   }
+  const bool sure = fabsf(first) == INFINITY;
+  bool tight = fabsf(score) == INFINITY && !sure && g < a.n_group;
+  if (sure) off = 0.f;
   const float near = off + warp_fmax(g < a.n_group ? off : 0.f);  // with any other group's
   int before = 0;
   uint32_t close = 0;
   for (int i = 0; i < a.n_group; ++i) {
     const float o = __shfl_sync(0xffffffffu, score, i * per);
     before += o > score || (o == score && i < g);
-    if (approximate && fabsf(o - score) <= near) close |= 1u << i;
+    if (approximate && fabsf(o - score) <= near) close |= 1u << i;  // two infinities are not: NaN
   }
   const bool mine = g < a.n_group && before < a.topk_group;
   uint32_t k = __ballot_sync(0xffffffffu, mine && s == 0), m = 0;
   for (int i = 0; i < a.n_group; ++i) m |= (k >> (i * per) & 1u) << i;
   *keep = m;
-  const bool tight = g < a.n_group && (close & (mine ? ~m : m)) != 0;
+  tight |= g < a.n_group && (close & (mine ? ~m : m)) != 0;
   return !__any_sync(0xffffffffu, tight);
 }
 
@@ -488,7 +492,7 @@ __device__ __forceinline__ void finish_tokens(const RouterArgs& a, const V* __re
     // A score of 1 bounds every error.  Between two chosen ones the errors of their own scores decide where that is not
     // enough (one that overtakes several lies within them of the one before it); behind the last one stand experts whose
     // keys are not at hand, so there any score has to be allowed for.
-    tight = next && key1 != -INFINITY &&
+    tight = next && key1 != -INFINITY && key0 != INFINITY &&  // infinite keys are so in truth
             key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1);
     if (tight && k + 1 < a.K) {
       const float b0 = bias[id], b1 = bias[e1];
