@@ -254,6 +254,28 @@ def test_micro_batches_that_are_each_reduced():
     assert float((got.double() - want).norm() / want.norm()) <= 1e-6
 
 
+def test_second_derivatives_are_refused():
+    """Rather than left out of a sum that has other parts."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    from token_dispatch_histogram_b200.autograd import ep_experts_fn, ep_router_fn
+    x = torch.randn(8, 16, device="cuda", requires_grad=True)
+    w, _ = ep_router_fn(x, 2)
+    (dx,) = torch.autograd.grad((w * w).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (dx.square().sum() + w.sum()).backward()
+    R, S, K, E, H, I = case = 2, 16, 2, 4, 64, 8
+    rows, logits, w13, w2, _ = make(*case)
+    layer = tdh.EpLayer(R, S, K, E, H, 4, grad_n=3 * H * I)
+    layer.router(logits)
+    layer.route()
+    rows = rows.repeat(2, 1).requires_grad_(True)
+    y = ep_experts_fn(rows, w13, w2, layer).float()
+    (dx,) = torch.autograd.grad(y.square().sum(), rows, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (dx.float().square().sum() + y.sum()).backward()
+
+
 @pytest.mark.parametrize("planner", ["exact", "quota"])
 def test_a_ranks_slots_cover_its_rows(planner):
     """Each rank's products over its own buffer, with home weights and prefetched replicas' weights, equal the rows of

@@ -23,10 +23,14 @@ for the backward pass ("ÎˆÎ½Î± ÏÎµÎ±Î»Î¹ÏƒÏ„Î¹ÎºÏŒ Ï€Î»Î±Î¯ÏƒÎ¹Î¿ Î±Î¾Î¹Î¿Î»ÏŒÎ
   plan's slots by reference: both must stay as they are until the backward (a
   buffer and a layer of their own, not the next step's).
 
+The gradients of ep_router_fn and ep_experts_fn have no graph of their own: one
+that would need it (create_graph) is refused.
+
 Every step runs in libep.so's kernels; these classes only allocate outputs and
 route tensors.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (ep_combine, ep_combine_backward, ep_dispatch, ep_dispatch_backward, ep_expert_gemm, ep_expert_up,
                ep_router, ep_router_backward)
@@ -80,6 +84,7 @@ class _Router(torch.autograd.Function):
         return w, ids
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dw, _):
         logits, ids = ctx.saved_tensors
         dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
@@ -101,6 +106,7 @@ class _Experts(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         rows, w13, w2, gu = ctx.saved_tensors
         dgu = torch.empty_like(gu)
