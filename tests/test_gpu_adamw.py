@@ -466,6 +466,29 @@ def test_a_refused_step_does_not_count():
     assert int(case.step) == 2
 
 
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_nan_changes_no_other_element_of_its_block(bits):
+    """Every other element, code and scale as if the element with the NaN had gradients of 0."""
+    case, clean = Case([256 * 4], bits), Case([256 * 4], bits)
+    case.g[0][300], clean.g[0][300] = float("nan"), 0.0
+    for c in (case, clean):
+        o = c.make(lr=1e-3)
+        o.step()
+        c.new_grads()
+        c.g[0][300] = 0.0
+        o.step()
+    a, b = case.numpy(), clean.numpy()
+    rest = np.arange(1024) != 300
+    for k in ("p", "m", "v"):
+        x, y = np.asarray(a[k][0]), np.asarray(b[k][0])
+        np.testing.assert_array_equal(x[rest], y[rest])
+        assert np.isnan(x[300]) if x.dtype == np.float32 else (x[300] & 0x7F) == 0x7F
+    if bits == 8:
+        np.testing.assert_array_equal(a["ms"][0], b["ms"][0])
+        np.testing.assert_array_equal(a["vs"][0], b["vs"][0])
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 
 def test_adamw_argument_errors():

@@ -338,6 +338,20 @@ def test_the_weight_gradient_keeps_32_bits_over_long_slots():
 
 
 @gpu
+def test_the_weight_gradient_sums_512_rows_at_a_time():
+    """One sign throughout: the accumulator cuts off up to 4.5e-9 of a partial sum for each of its 512 rows; the eight
+    partial sums are added with seven roundings, the j-th of a sum of j + 1 parts in 8 (half a unit, 2^-24, each)."""
+    import torch
+    import token_dispatch_histogram_b200 as tdh
+    P = 4096
+    a, b = values((P, 64), 1).abs() + 0.5, values((P, 64), 2).abs() + 0.5
+    g = torch.empty((1, 64, 64), device="cuda")
+    tdh.ep_expert_wgrad(a, b, torch.tensor([0, P], dtype=torch.int32, device="cuda"), g)
+    want = a.double().T @ b.double()
+    assert torch.all((g[0].double() - want).abs() <= (512 * 4.5e-9 + 35 / 8 * 2.0 ** -24) * want)
+
+
+@gpu
 def test_slots_that_do_not_fit_are_left_out_and_flagged():
     import torch
     import token_dispatch_histogram_b200 as tdh

@@ -620,6 +620,34 @@ def test_groups_of_infinite_keys(score, group_top):
             np.testing.assert_array_equal(ids, want_ids)
 
 
+@gpu
+@pytest.mark.parametrize("T,E", [(64, 384), (4864, 384), (64, 1024), (4864, 96)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_an_expert_of_low_bias_and_high_score_at_the_border(score, T, E):
+    """The last chosen expert and the next ones are held up by their biases, and behind them stands one of a score near
+    1 and a low bias, whose key passes theirs, or does not, by less than its score's error in fp32."""
+    import torch
+    K = 8
+    rng = np.random.default_rng(E)
+    x = 0.1 * rng.standard_normal(E)
+    x[7] = 9.0 if score == "softmax" else 4.0
+    x = x.astype(np.float32)
+    s = ref_scores(x.astype(np.float64), score)
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    key = np.sort(np.delete(s + bias, 7))[::-1]
+    # keys within a few 1e-8 around the border
+    at = np.argsort(-np.where(np.arange(E) == 7, -9.0, s + bias))[K - 1:K + 2]
+    bias[at] = (key[K - 1] - s[at] + np.array([0.0, -3e-8, -6e-8])).astype(np.float32)
+    bias[7] = np.float32(key[K - 1] - s[7])
+    rows = np.repeat(x[None], T, 0)
+    rows[:, 7] += (np.arange(T) % 16 - 8) * np.float32(2.0 ** -19)  # a few units of the last place
+    kw = dict(score=score)
+    ids, w, st = call(torch.from_numpy(rows).cuda(), K, bias=bias, **kw)
+    want_ids, want = ref_router(rows[:16].astype(np.float64), K, bias=bias.astype(np.float64), **kw)
+    assert len({tuple(r) for r in want_ids}) > 1  # 7 among them or not
+    np.testing.assert_array_equal(ids, np.tile(want_ids, (T // 16, 1)))
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 
 def test_router_argument_errors():
