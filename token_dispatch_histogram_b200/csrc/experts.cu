@@ -23,11 +23,12 @@
 // accumulator into registers, give it back, and bring it through the epilogue to
 // global memory while the next tile's products run.
 //
-// Measured (B200, after a pause): second projection of 32,768 rows in 13 slots, H
-// 7168, I 2048, 676 us = 1424 TFLOP/s (the library's product of one such matrix 627);
-// first projection of 196,608 rows in 64 slots, H 2048, I 1024, its products kept,
-// 1240 us = 1330; weight gradient of the same 705 us = 1170; backward of the activation
-// at the first size 800 us = 1203.  In a loop the power cap takes 10 % off all of them.
+// Measured (B200; one call at a time with a flush of L2 between, and in a loop over new inputs, where the power cap takes
+// its part): first projection of 196,608 rows in 64 slots, H 2048, I 1024, its products kept, 1253 us = 1316 TFLOP/s, in a
+// loop 1450 to 1540; weight gradient of the same 668 to 683 us = 1220, 800 to 850; second projection of 32,768 rows in 13
+// slots, H 7168, I 2048, 757 us = 1270, 773 to 813; backward of the activation there 803 us = 1197, 930 to 970.  The
+// library's product of one dense matrix of the second projection's size takes 627 us after a pause and 700 in a loop: a
+// bound to compare with, not the same work.
 //
 // A tile's rows are its slot's rows from a multiple of 256 on; rows behind the
 // slot's end belong to the next slot and only make accumulator rows that are
@@ -36,10 +37,11 @@
 // that an infinity or NaN of the next slot takes no part) by warp 3.
 //
 // The accumulator's additions cut off rather than round: over n rows of one sign
-// the sum comes out about n * 4.5e-9 too small (measured: 1.0e-5 at 4096 rows,
+// the sum comes out up to n * 4.5e-9 too small (measured: 1.0e-5 at 4096 rows,
 // 7.4e-5 at 16,384).  bf16 results do not see that; the weight gradient is fp32
 // and may run over a hundred thousand rows, so it takes the accumulator out
-// every 512 rows (4e-7) and adds these partial sums in registers.
+// every 512 rows (6e-7 at most of one sign, whatever the slot's length) and adds
+// these partial sums in registers.
 #include <cuda.h>
 
 #include "umma.cuh"
@@ -1049,9 +1051,14 @@ static int launch_few(const CUtensorMap& mx, const CUtensorMap& mw, ExpertArgs a
   return EP_OK;
 }
 
-// Few rows to a slot on average: then the weights' bytes are what counts.  Up over 64 experts (H 2048, I 1024), us wide /
-// few: 8 rows a slot 106 / 93, 32 rows 109 / 94, 64 rows 112 / 139.  But the host knows the average only; with all rows in
-// one slot: 8 a slot 26 / 26, 16 a slot 29 / 49, 32 a slot 27 / 78.  Up to 8 it never costs.
+// Few rows to a slot on average: then the weights' bytes are what counts.  Rows spread evenly, us wide / few:
+//   up, 64 experts, H 2048, I 1024      1 to 8 rows a slot 100 / 90   32: 102 / 92   64: 104 / 109
+//   second projection of the same                1 to 8: 55 / 53          32: 57 / 55    64: 59 / 72
+//   8 experts, H 7168, I 2048                    1 to 8: 55 / 47 to 49    32: 55 / 51    64: 57 / 74
+//   64 experts, H 7168, I 2048                   1 to 8: 305 to 315 / 274 to 283  32: 324 / 291  64: 330 / 420
+// The host knows the average only.  With all rows in one slot an average of 8 costs nothing or little in the first three
+// (up 26 / 26; 18 / 18; 23 / 27) and 25 / 74 in the last (512 rows of one expert), one of 16 costs 29 / 49, 18 / 27, 25 / 27
+// and 35 / 123: so up to 8.  The other forms have no such variant.
 static bool few_rows(int64_t rows, int n_slots, int n_w) { return rows <= 8 * (int64_t)(n_slots < n_w ? n_slots : n_w); }
 
 template <Form F>

@@ -14,8 +14,10 @@
 //
 // Which of two experts comes first is decided by numbers that can lie closer
 // than 32-bit scores tell apart, so keys and group scores are held in 64 bits.
-// The weights are 32-bit: each is a ratio of exponentials of differences of the
-// chosen logits, exact to a few units in the last place at any magnitude.
+// The weights are 32-bit ratios of exponentials of differences of logits: off by
+// 2^-24 of the difference's size (its rounding) and a few units in the last place
+// besides; without renorm a softmax divides by a sum of approximated exponentials
+// (2^-22 of each), some units more.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -491,7 +493,9 @@ __device__ __forceinline__ void finish_tokens(const RouterArgs& a, const V* __re
     bool tight = false;
     // A score of 1 bounds every error.  Between two chosen ones the errors of their own scores decide where that is not
     // enough (one that overtakes several lies within them of the one before it); behind the last one stand experts whose
-    // keys are not at hand, so there any score has to be allowed for.
+    // keys are not at hand, so there any score has to be allowed for.  With a softmax that is wide against keys of about
+    // 1 / E: 524,288 tokens over 384 experts, K = 8, take 507 us where logits spread by 1 (284 without a bias) and 961 where
+    // they spread by 0.3; 262,144 over 1024 experts 870 and 2260 (278).
     tight = next && key1 != -INFINITY && key0 != INFINITY &&  // infinite keys are so in truth
             key0 - key1 <= key_error(a.sigmoid, 1.f, key0) + key_error(a.sigmoid, 1.f, key1);
     if (tight && k + 1 < a.K) {
