@@ -458,9 +458,9 @@ def test_weight_gradients_of_the_largest_ids(n_slots):
     lens = [int(v) for v in np.random.default_rng(n_slots).integers(0, 5, n_slots)]
     buf = Buffer(lens, replicas=False)
     a, b = values((buf.P, M), 1, True), values((buf.P, N), 2, True)
-    # the highest ids, and those 3072 below them
+    # the highest ids, and as many below them as the slots of a call, in whole words of 32
     high = E + cap - 1 - np.arange(n_slots - n_slots // 2)
-    order = np.concatenate([high[:n_slots // 2] - 3072, high]).astype(np.int32)
+    order = np.concatenate([high[:n_slots // 2] - (cap + 31) // 32 * 32, high]).astype(np.int32)
     for twice in (False, True):
         if twice:
             order[3] = order[n_slots - 1]
